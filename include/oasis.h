@@ -345,6 +345,100 @@ int oasis_sparse_attn(const oasis_dims* d, const void* q, const void* pool,
                       const int32_t* slot_table, const int32_t* ctx_len, float scale,
                       float* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- draft trees ----------------------------------------------------------
+ * One speculative step over this cache.  The target model runs once over the
+ * T = n_tree nodes of a tree of drafted tokens per sequence (1 <= T <= 64);
+ * node 0, the root, is the last token already decided, whose keys and values
+ * are not in the cache yet.  parent[b][j] < j names a node's parent (-1: a
+ * root).  n_nodes[b] <= T real nodes a sequence, NULL: T everywhere; the nodes
+ * behind them are padding.  The step, in stream order: oasis_tree_layout once,
+ * then per layer oasis_qk_norm_rope and oasis_tree_attn, then
+ * oasis_verify_tree once and oasis_commit_path once for every layer.  dims
+ * gives the batch, heads and cache sizes; n_queries is not used.
+ *   q       bf16 [B][T][Hq][D]            k_tree, v_tree  bf16 [B][Hkv][T][D]
+ *   mask    uint64 [B][T]: bit i of mask[b][j] is set if node j sees node i */
+
+/* Visibility words and positions of a tree's nodes from their parents:
+ *   mask[b][j] = bit j | mask[b][parent[b][j]],  pos[b][j] = ctx_len[b] + depth of j
+ * (a root has depth 0).  Padding nodes: mask 0, pos ctx_len[b].  A parent
+ * outside [-1, j) is taken as -1, n_nodes outside [0, T] as the nearer end;
+ * both set OASIS_DEVERR_ID_RANGE.  All device: parent int32 [B][T], n_nodes
+ * int32 [B], mask uint64 [B][T], pos int32 [B][T]. */
+int oasis_tree_layout(const oasis_dims* d, int32_t n_tree, const int32_t* parent, const int32_t* n_nodes,
+                      const int32_t* ctx_len, uint64_t* mask, int32_t* pos, void* stream);
+
+/* Query rows, keys and values from the rows of a fused projection: RMS norm of
+ * each query and key head (weights wq, wk: bf16 [D], NULL: no norm), then the
+ * rotation of channel pairs (i, i + 64) by pos * inv_freq[i]; values are
+ * copied.  qkv: bf16, B * n_tok rows, row_stride elements apart (a multiple of
+ * 8), each Hq query heads, Hkv key heads, Hkv value heads of D.  inv_freq:
+ * fp32 [64]; pos: int32 [B][n_tok].  Angles are reduced in fp64, norm and
+ * rotation computed in fp32 and rounded once to bf16.  Writes q bf16
+ * [B][n_tok][Hq][D] and k, v bf16 [B][Hkv][n_tok][D], which must not overlap
+ * qkv.  n_tok is any number of tokens >= 1 (a tree's nodes or a prompt's
+ * chunk).  All device. */
+int oasis_qk_norm_rope(const oasis_dims* d, int32_t n_tok, const void* qkv, size_t row_stride, const void* wq,
+                       const void* wk, float eps, const float* inv_freq, const int32_t* pos, void* q, void* k, void* v,
+                       void* stream);
+
+/* Workspace bytes of oasis_tree_attn (0 for bad dims).  Device memory that
+ * must be zero-filled once before its first use; the kernel leaves it ready
+ * for the next call.  Calls on one workspace must be stream-ordered. */
+size_t oasis_tree_workspace_bytes(const oasis_dims* d, int32_t n_tree);
+
+/* Attention of a tree's nodes over the resident pool slots (as
+ * oasis_sparse_attn) and over the nodes of the tree itself: the row of node j
+ * sees every valid token of every occupied slot and the nodes whose bits are
+ * set in mask[b][j] (any words; bits at or above T are ignored).  A row whose
+ * word is 0 sees nothing: out = 0, lse = -inf.  Infinities and NaN in nodes
+ * that a row does not see do not reach it.  Softmax statistics and sums are
+ * fp32; out is rounded once to bf16.  q, k_tree, v_tree, mask as above; out
+ * bf16 [B][T][Hq][D]; lse fp32 [B][T][Hq] (natural log).  Hq / Hkv <= 64.
+ * All device; ws: oasis_tree_workspace_bytes(d, n_tree) bytes. */
+int oasis_tree_attn(const oasis_dims* d, int32_t n_tree, const void* q, const void* pool, const int32_t* slot_table,
+                    const int32_t* ctx_len, const void* k_tree, const void* v_tree, const uint64_t* mask, float scale,
+                    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Which drafted tokens stand (rejection sampling down the tree), from given
+ * random numbers.  probs[b][j]: the target's probabilities after node j, fp32,
+ * rows of `vocab` entries row_stride apart; draft_probs[b][j]: those that the
+ * children of node j were drawn from, same layout, or NULL when they were not
+ * drawn at random.  From the root on, the children of the current node c are
+ * tested in index order, with r = probs[b][c], d = draft_probs[b][c], S = 1:
+ *   child j with token x stands if r(x) > 0 and u_accept[b][j] * S * d(x) < r(x);
+ *   otherwise r <- max(r - S * d, 0) and S <- sum of r.
+ * Without draft_probs d(x) is 1, and a rejection makes S <- S - r(x),
+ * r(x) <- 0.  When no child stands, next_token is drawn from r: the first index
+ * whose running sum passes max(u_sample[b], 0) * (sum of r); if nothing is left
+ * of r, from probs[b][c]; -1 if that has no mass either.  Sums are fp64;
+ * entries that are not positive finite numbers count as 0.  u_accept [B][T],
+ * u_sample [B]: fp32, in [0, 1).  tokens, parent: int32 [B][T].  Writes path
+ * int32 [B][T] (the nodes that stand, root first, -1 padded), n_accept int32
+ * [B] (how many: the root counts) and next_token int32 [B]; a sequence without
+ * nodes gets 0 and -1.  A node whose token is outside [0, vocab) or whose
+ * parent is outside [-1, j) never stands and sets OASIS_DEVERR_ID_RANGE.  All
+ * device. */
+int oasis_verify_tree(const oasis_dims* d, int32_t n_tree, int32_t vocab, const float* probs, const float* draft_probs,
+                      size_t row_stride, const int32_t* tokens, const int32_t* parent, const int32_t* n_nodes,
+                      const float* u_accept, const float* u_sample, int32_t* path, int32_t* n_accept,
+                      int32_t* next_token, void* stream);
+
+/* The accepted nodes' keys and values into the cache of n_layers layers at
+ * once (oasis_append_kv for a whole path and stack).  Node path[b][i],
+ * i < n_accept[b], goes to position ctx_len[b] + i of every layer: into
+ * host_kv (mapped host; NULL skips it), into the pool slot that holds the
+ * block if it is resident (pool NULL skips it), and into kmin / kmax (a path
+ * that opens a block starts its summary).  Of each oasis_layer only host_kv,
+ * kmin, kmax, pool and slot_table are used; they are written (slot_table is
+ * only read, and needs only its 4-byte alignment).  layers: host array.  k_tree, v_tree: bf16
+ * [n_layers][B][Hkv][T][D].  If ctx_len_out is not NULL, ctx_len_out[b] =
+ * ctx_len[b] + rows written (it must not alias ctx_len).  Positions at or
+ * beyond N*P set OASIS_DEVERR_APPEND_FULL, path entries outside [0, T) and
+ * n_accept outside [0, T] OASIS_DEVERR_ID_RANGE; such rows are skipped. */
+int oasis_commit_path(const oasis_dims* d, int32_t n_tree, const oasis_layer* layers, int32_t n_layers,
+                      const void* k_tree, const void* v_tree, const int32_t* path, const int32_t* n_accept,
+                      const int32_t* ctx_len, int32_t* ctx_len_out, void* stream);
+
 /* Reads (and if clear != 0 resets) this device's error word; synchronises
  * `stream`.  For tests and diagnostics, not for the hot loop. */
 int oasis_read_device_error(uint32_t* out, int clear, void* stream);

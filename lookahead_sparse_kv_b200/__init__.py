@@ -107,6 +107,16 @@ _SIGS = {
     "oasis_prefetch": (ctypes.c_int, [ctypes.POINTER(Dims), _V, _V, _V, _V, _V, _V]),
     "oasis_sparse_attn": (ctypes.c_int, [ctypes.POINTER(Dims), _V, _V, _V, _V, ctypes.c_float,
                                          _V, _V, _V, ctypes.c_size_t, _V]),
+    "oasis_tree_layout": (ctypes.c_int, [ctypes.POINTER(Dims), _I32, _V, _V, _V, _V, _V, _V]),
+    "oasis_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(Dims), _I32, _V, ctypes.c_size_t, _V, _V, ctypes.c_float, _V, _V,
+                                          _V, _V, _V, _V]),
+    "oasis_tree_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Dims), _I32]),
+    "oasis_tree_attn": (ctypes.c_int, [ctypes.POINTER(Dims), _I32, _V, _V, _V, _V, _V, _V, _V, ctypes.c_float, _V, _V, _V,
+                                       ctypes.c_size_t, _V]),
+    "oasis_verify_tree": (ctypes.c_int, [ctypes.POINTER(Dims), _I32, _I32, _V, _V, ctypes.c_size_t, _V, _V, _V, _V, _V, _V,
+                                         _V, _V, _V]),
+    "oasis_commit_path": (ctypes.c_int, [ctypes.POINTER(Dims), _I32, ctypes.POINTER(Layer), _I32, _V, _V, _V, _V, _V, _V,
+                                         _V]),
     "oasis_read_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int, _V]),
     "oasis_check_dims": (ctypes.c_int, [ctypes.POINTER(Dims)]),
     "oasis_last_error": (ctypes.c_char_p, []),
@@ -435,3 +445,16 @@ def read_device_error(clear: bool = True, stream=None) -> int:
     _check(lib().oasis_read_device_error(ctypes.byref(v), int(clear), _stream(stream)),
            "oasis_read_device_error")
     return v.value
+
+
+_TREE_CALLS = ("tree_layout", "qk_norm_rope", "tree_workspace_bytes", "tree_attn", "verify_tree", "make_cache_layers",
+               "commit_path")
+
+
+def __getattr__(name):
+    """The draft-tree calls (tree.py), loaded with torch when the first of them is asked for."""
+    if name in _TREE_CALLS:
+        from . import tree
+        globals().update({n: getattr(tree, n) for n in _TREE_CALLS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

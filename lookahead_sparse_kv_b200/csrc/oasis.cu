@@ -23,9 +23,12 @@
 #include "overlap.cuh"
 #include "plan.cuh"
 #include "prefetch.cuh"
+#include "qkrope.cuh"
 #include "score.cuh"
 #include "select.cuh"
 #include "summaries.cuh"
+#include "tree.cuh"
+#include "verify.cuh"
 
 namespace {
 
@@ -794,3 +797,5 @@ int oasis_score_select_noalloc(const oasis_dims* dp, const void* q, const void* 
 }
 
 }  // extern "C"
+
+#include "tree_api.cuh"

@@ -1,0 +1,276 @@
+// tree_api.cuh - C entry points of the draft-tree calls (part of oasis.cu).
+
+namespace {
+
+// Launch attributes of a kernel set once per device instead of on every call.
+struct OncePerDevice {
+    std::mutex mu;
+    uint64_t done = 0;
+    template <class F>
+    int operator()(F&& f) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev < 64 && (done >> dev & 1)) return OASIS_OK;
+        if (int rc = f()) return rc;
+        if (dev < 64) done |= 1ull << dev;
+        return OASIS_OK;
+    }
+};
+
+int check_tree(const oasis_dims* dp, int32_t n_tree, Dims* d) {
+    if (int rc = validate(dp, d)) return rc;
+    if (n_tree < 1 || n_tree > oasis::kMaxTree)
+        return fail(OASIS_EINVAL, "n_tree must be in [1, 64] (got %d)", n_tree);
+    return OASIS_OK;
+}
+
+// The tree's keys or values: bf16 [B*Hkv][T][128] as a 3-D tensor, boxes of
+// 64 columns x the nodes padded to whole slots; rows past T read as zeros.
+int make_map_tree(CUtensorMap* m, const void* base, unsigned long long units, int T, const char* name) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return fail(OASIS_ECUDA, "cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(oasis::kHeadDim), static_cast<cuuint64_t>(T),
+                                static_cast<cuuint64_t>(units)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(oasis::kRowBytes),
+                                   static_cast<cuuint64_t>(oasis::kRowBytes) * T};
+    const int t16 = (T + oasis::kBlockTokens - 1) / oasis::kBlockTokens * oasis::kBlockTokens;
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(t16), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(OASIS_ECUDA, "cuTensorMapEncodeTiled(%s) failed: %d", name, static_cast<int>(r));
+    return OASIS_OK;
+}
+
+// Nodes of one launch: as many as 64 query rows hold.
+Dims tree_dims(const Dims& d, int T) {
+    Dims t = d;
+    t.Qn = std::min(T, 64 / d.G());
+    return t;
+}
+
+int check_tree_heads(const Dims& d) {
+    if (d.G() > 64) return fail(OASIS_EINVAL, "n_q_heads / n_kv_heads must be <= 64 (got %d)", d.G());
+    return OASIS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int oasis_tree_layout(const oasis_dims* dp, int32_t n_tree, const int32_t* parent, const int32_t* n_nodes,
+                      const int32_t* ctx_len, uint64_t* mask, int32_t* pos, void* stream) {
+    Dims d;
+    if (int rc = check_tree(dp, n_tree, &d)) return rc;
+    if (int rc = check_ptr(parent, "parent")) return rc;
+    if (int rc = check_ptr(n_nodes, "n_nodes", true)) return rc;
+    if (int rc = check_ptr(ctx_len, "ctx_len")) return rc;
+    if (int rc = check_ptr(mask, "mask")) return rc;
+    if (int rc = check_ptr(pos, "pos")) return rc;
+    static OncePerDevice once;
+    if (int rc = once([] { return carveout(oasis::tree_layout_kernel, "tree_layout carve-out"); })) return rc;
+    const unsigned grid = (d.B + oasis::kLayoutTrees - 1) / oasis::kLayoutTrees;
+    oasis::tree_layout_kernel<<<grid, oasis::kLayoutTrees * oasis::kMaxTree, 0, static_cast<cudaStream_t>(stream)>>>(
+        d.B, n_tree, parent, n_nodes, ctx_len, mask, pos);
+    return check_launch("tree_layout launch");
+}
+
+int oasis_qk_norm_rope(const oasis_dims* dp, int32_t n_tok, const void* qkv, size_t row_stride, const void* wq,
+                       const void* wk, float eps, const float* inv_freq, const int32_t* pos, void* q, void* k, void* v,
+                       void* stream) {
+    Dims d;
+    if (int rc = validate(dp, &d)) return rc;
+    if (n_tok < 1) return fail(OASIS_EINVAL, "n_tok must be >= 1 (got %d)", n_tok);
+    if (int rc = check_ptr(qkv, "qkv")) return rc;
+    if (int rc = check_ptr(wq, "wq", true)) return rc;
+    if (int rc = check_ptr(wk, "wk", true)) return rc;
+    if (int rc = check_ptr(inv_freq, "inv_freq")) return rc;
+    if (int rc = check_ptr(pos, "pos")) return rc;
+    if (int rc = check_ptr(q, "q")) return rc;
+    if (int rc = check_ptr(k, "k")) return rc;
+    if (int rc = check_ptr(v, "v")) return rc;
+    const int heads = d.Hq + 2 * d.Hkv;
+    if (row_stride < static_cast<size_t>(heads) * oasis::kHeadDim || row_stride % 8 != 0 || row_stride > (size_t(1) << 40))
+        return fail(OASIS_EINVAL, "row_stride must be a multiple of 8 and >= (Hq + 2 Hkv) * 128 (got %zu)", row_stride);
+    if (!(eps >= 0.f) || !(eps < 3.0e38f)) return fail(OASIS_EINVAL, "eps must be a finite float >= 0");
+    static OncePerDevice once;
+    if (int rc = once([] { return carveout(oasis::qk_norm_rope_kernel, "qk_norm_rope carve-out"); })) return rc;
+    // Warps a token: one while there are enough tokens to fill the SMs (its
+    // angles are then made once), more when there are few.
+    const long long tokens = static_cast<long long>(d.B) * n_tok;
+    const int steps = (heads + oasis::kRopeStep - 1) / oasis::kRopeStep;
+    const long long fill = 32ll * sm_count();
+    const int split = static_cast<int>(std::min<long long>(steps, std::max<long long>(1, fill / tokens)));
+    const long long grid = (tokens * split + oasis::kRopeWarps - 1) / oasis::kRopeWarps;
+    if (grid > 0x7FFFFFFFll) return fail(OASIS_EINVAL, "too many tokens");
+    oasis::qk_norm_rope_kernel<<<static_cast<unsigned>(grid), oasis::kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        d, n_tok, split, static_cast<const uint16_t*>(qkv), static_cast<long long>(row_stride), static_cast<const uint16_t*>(wq),
+        static_cast<const uint16_t*>(wk), eps, inv_freq, pos, static_cast<uint16_t*>(q), static_cast<uint16_t*>(k),
+        static_cast<uint16_t*>(v));
+    return check_launch("qk_norm_rope launch");
+}
+
+size_t oasis_tree_workspace_bytes(const oasis_dims* dp, int32_t n_tree) {
+    Dims d;
+    if (check_tree(dp, n_tree, &d) != OASIS_OK || check_tree_heads(d) != OASIS_OK) return 0;
+    return ws_layout(tree_dims(d, n_tree)).total;
+}
+
+int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const void* pool, const int32_t* slot_table,
+                    const int32_t* ctx_len, const void* k_tree, const void* v_tree, const uint64_t* mask, float scale,
+                    void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    Dims full;
+    if (int rc = check_tree(dp, n_tree, &full)) return rc;
+    if (int rc = check_tree_heads(full)) return rc;
+    if (int rc = check_ptr(q, "q")) return rc;
+    if (int rc = check_ptr(pool, "pool")) return rc;
+    if (int rc = check_ptr(slot_table, "slot_table")) return rc;
+    if (int rc = check_ptr(ctx_len, "ctx_len")) return rc;
+    if (int rc = check_ptr(k_tree, "k_tree")) return rc;
+    if (int rc = check_ptr(v_tree, "v_tree")) return rc;
+    if (int rc = check_ptr(mask, "mask")) return rc;
+    if (int rc = check_ptr(out, "out")) return rc;
+    if (int rc = check_ptr(lse, "lse")) return rc;
+    if (int rc = check_ptr(ws, "ws")) return rc;
+    if (!(scale > 0.f) || !(scale < 3.0e38f)) return fail(OASIS_EINVAL, "scale must be a positive finite float");
+    Dims d = tree_dims(full, n_tree);
+    const WsLayout w = ws_layout(d);
+    if (ws_bytes < w.total) return fail(OASIS_EINVAL, "workspace too small: %zu < %zu", ws_bytes, w.total);
+    CUtensorMap tk, tv, tq, ttk, ttv;
+    const unsigned long long units = static_cast<unsigned long long>(d.B) * d.Hkv;
+    if (int rc = make_map_pool(&tk, pool, units * d.K, "pool keys")) return rc;
+    if (int rc = make_map_pool(&tv, static_cast<const uint8_t*>(pool) + oasis::kBlockBytes / 2, units * d.K, "pool values"))
+        return rc;
+    if (int rc = make_map_tree(&ttk, k_tree, units, n_tree, "tree keys")) return rc;
+    if (int rc = make_map_tree(&ttv, v_tree, units, n_tree, "tree values")) return rc;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    float* ws_lse = reinterpret_cast<float*>(base + w.lse);
+    float* ws_o = reinterpret_cast<float*>(base + w.o);
+    int* ws_ticket = reinterpret_cast<int*>(base + w.ticket);
+    int* ws_sched = reinterpret_cast<int*>(base + w.sched);
+    const float scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int per = d.Qn;
+    for (int j0 = 0; j0 < n_tree; j0 += per) {
+        d.Qn = std::min(per, n_tree - j0);
+        Dims dq = d;
+        dq.Qn = n_tree;
+        if (int rc = make_map_q(&tq, q, dq, d.Qn)) return rc;
+        const oasis::AttnChunks chunks = attn_chunks(d, sm_count());
+        const int grid_max = std::max(1, sm_count() - oasis::kPrefetchCtas);
+        const unsigned ctas = static_cast<unsigned>(std::min(grid_max, chunks.nc));
+        const bool r32 = d.Qn * d.G() <= 32;
+        auto kern = r32 ? oasis::tree_attn_kernel<32> : oasis::tree_attn_kernel<64>;
+        const int smem = oasis::attn_smem(r32 ? 32 : 64, true);
+        static OncePerDevice once[2];
+        if (int rc = once[r32]([&] { return set_smem(kern, smem, "tree_attn smem"); })) return rc;
+        const oasis::AttnTree tr{mask, static_cast<const uint16_t*>(v_tree), n_tree, j0};
+        kern<<<ctas, oasis::kAttnThreads, smem, s>>>(tk, tv, tq, ttk, ttv, tr, d, slot_table, ctx_len, scale_log2, chunks,
+                                                     static_cast<__nv_bfloat16*>(out), lse, ws_o, ws_lse, ws_ticket, ws_sched);
+        if (int rc = check_launch("tree_attn launch")) return rc;
+    }
+    return OASIS_OK;
+}
+
+int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const float* probs, const float* draft_probs,
+                      size_t row_stride, const int32_t* tokens, const int32_t* parent, const int32_t* n_nodes,
+                      const float* u_accept, const float* u_sample, int32_t* path, int32_t* n_accept,
+                      int32_t* next_token, void* stream) {
+    Dims d;
+    if (int rc = check_tree(dp, n_tree, &d)) return rc;
+    if (vocab < 1 || vocab > (1 << 30)) return fail(OASIS_EINVAL, "vocab must be in [1, 2^30] (got %d)", vocab);
+    if (row_stride < static_cast<size_t>(vocab) || row_stride > (size_t(1) << 40))
+        return fail(OASIS_EINVAL, "row_stride must be >= vocab (got %zu)", row_stride);
+    if (int rc = check_ptr(probs, "probs")) return rc;
+    if (int rc = check_ptr(draft_probs, "draft_probs", true)) return rc;
+    if (int rc = check_ptr(tokens, "tokens")) return rc;
+    if (int rc = check_ptr(parent, "parent")) return rc;
+    if (int rc = check_ptr(n_nodes, "n_nodes", true)) return rc;
+    if (int rc = check_ptr(u_accept, "u_accept")) return rc;
+    if (int rc = check_ptr(u_sample, "u_sample")) return rc;
+    if (int rc = check_ptr(path, "path")) return rc;
+    if (int rc = check_ptr(n_accept, "n_accept")) return rc;
+    if (int rc = check_ptr(next_token, "next_token")) return rc;
+    static OncePerDevice once;
+    if (int rc = once([] { return carveout(oasis::verify_tree_kernel, "verify_tree carve-out"); })) return rc;
+    oasis::VerifyArgs a;
+    a.probs = probs;
+    a.draft = draft_probs;
+    a.tokens = tokens;
+    a.parent = parent;
+    a.n_nodes = n_nodes;
+    a.u_accept = u_accept;
+    a.u_sample = u_sample;
+    a.path = path;
+    a.n_accept = n_accept;
+    a.next_token = next_token;
+    a.row_stride = static_cast<long long>(row_stride);
+    a.B = d.B;
+    a.T = n_tree;
+    a.vocab = vocab;
+    oasis::verify_tree_kernel<<<static_cast<unsigned>(d.B) * oasis::kVerCluster, oasis::kVerThreads, 0,
+                                static_cast<cudaStream_t>(stream)>>>(a);
+    return check_launch("verify_tree launch");
+}
+
+int oasis_commit_path(const oasis_dims* dp, int32_t n_tree, const oasis_layer* layers, int32_t n_layers,
+                      const void* k_tree, const void* v_tree, const int32_t* path, const int32_t* n_accept,
+                      const int32_t* ctx_len, int32_t* ctx_len_out, void* stream) {
+    Dims d;
+    if (int rc = check_tree(dp, n_tree, &d)) return rc;
+    if (layers == nullptr) return fail(OASIS_EINVAL, "layers is NULL");
+    if (n_layers < 1) return fail(OASIS_EINVAL, "n_layers must be >= 1 (got %d)", n_layers);
+    if (int rc = check_ptr(k_tree, "k_tree")) return rc;
+    if (int rc = check_ptr(v_tree, "v_tree")) return rc;
+    if (int rc = check_ptr(path, "path")) return rc;
+    if (int rc = check_ptr(n_accept, "n_accept")) return rc;
+    if (int rc = check_ptr(ctx_len, "ctx_len")) return rc;
+    if (int rc = check_ptr(ctx_len_out, "ctx_len_out", true)) return rc;
+    if (ctx_len_out != nullptr && ctx_len_out == ctx_len)
+        return fail(OASIS_EINVAL, "ctx_len_out must not alias ctx_len");
+    // every layer is checked before the first launch
+    for (int i = 0; i < n_layers; ++i) {
+        const oasis_layer& L = layers[i];
+        if (int rc = check_ptr(L.host_kv, "host_kv", true)) return rc;
+        if (int rc = check_ptr(L.kmin, "kmin")) return rc;
+        if (int rc = check_ptr(L.kmax, "kmax")) return rc;
+        if (int rc = check_ptr(L.pool, "pool", true)) return rc;
+        if (L.pool != nullptr && L.slot_table == nullptr) return fail(OASIS_EINVAL, "slot_table is NULL");
+        // (read an entry at a time: a layer's slice of a stacked table starts anywhere)
+        if (L.pool != nullptr && reinterpret_cast<uintptr_t>(L.slot_table) % 4 != 0)
+            return fail(OASIS_EINVAL, "slot_table is not 4-byte aligned");
+        const void* hv = nullptr;
+        if (L.host_kv != nullptr)
+            if (int rc = device_view(L.host_kv, "host_kv", false, &hv)) return rc;
+    }
+    static OncePerDevice once;
+    if (int rc = once([] { return carveout(oasis::commit_path_kernel, "commit_path carve-out"); })) return rc;
+    const size_t layer_rows = static_cast<size_t>(d.B) * d.Hkv * n_tree;
+    for (int l0 = 0; l0 < n_layers; l0 += oasis::kCommitLayers) {
+        const int nl = std::min(n_layers - l0, oasis::kCommitLayers);
+        oasis::CommitLayers c = {};
+        for (int i = 0; i < nl; ++i) {
+            const oasis_layer& L = layers[l0 + i];
+            const void* hv = nullptr;
+            if (L.host_kv != nullptr)
+                if (int rc = device_view(L.host_kv, "host_kv", false, &hv)) return rc;
+            c.host[i] = static_cast<uint4*>(const_cast<void*>(hv));
+            c.pool[i] = static_cast<uint4*>(L.pool);
+            c.kmin[i] = static_cast<uint4*>(const_cast<void*>(L.kmin));
+            c.kmax[i] = static_cast<uint4*>(const_cast<void*>(L.kmax));
+            c.slot_table[i] = L.slot_table;
+        }
+        const dim3 grid(static_cast<unsigned>(d.B * d.Hkv), static_cast<unsigned>(nl));
+        oasis::commit_path_kernel<<<grid, oasis::kCommitThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+            c, d, n_tree, static_cast<const uint4*>(k_tree) + l0 * layer_rows * 16,
+            static_cast<const uint4*>(v_tree) + l0 * layer_rows * 16, path, n_accept, ctx_len,
+            l0 == 0 ? ctx_len_out : nullptr);
+        if (int rc = check_launch("commit_path launch")) return rc;
+    }
+    return OASIS_OK;
+}
+
+}  // extern "C"
