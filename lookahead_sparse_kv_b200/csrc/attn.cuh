@@ -71,7 +71,7 @@ constexpr int kAttnHalf = kAttnTileTokens * 128;                   // one 64-col
 constexpr int kAttnStageBytes = 2 * kAttnHalf;                     // K (or V) of one tile
 constexpr int kAttnQHalf = 64 * 128;                               // 64 query rows x 128 B
 constexpr int kAttnMaxChunkTiles = 16;
-constexpr int kAttnInfoInts = 8 + 4 * (kAttnMaxChunkTiles + 1);    // chunk header + 4 ints per tile (and the tree's)
+constexpr int kAttnInfoInts = 8 + 4 * kAttnMaxChunkTiles;          // chunk header + 4 ints per tile
 constexpr int kAttnSoftmaxWarps = 8;                              // warps 0-7 (two per TMEM quadrant)
 constexpr int kAttnEpiWarp = 8;                                    // warps 8-11
 constexpr int kAttnLoaderWarp = 12, kAttnSWarp = 13, kAttnOWarp = 14, kAttnListerWarp = 15;
@@ -105,14 +105,8 @@ constexpr int kAttnOffQ = (kAttnOffThr + 2 * 64 * 4 + 1023) / 1024 * 1024;
 constexpr int attn_q_bufs(int nr) { return nr == 64 ? 1 : 2; }
 constexpr int attn_p_buf_bytes(int nr) { return (nr == 64 ? 2 : 1) * kAttnHalf; }
 constexpr int attn_off_p(int nr) { return kAttnOffQ + attn_q_bufs(nr) * 2 * kAttnQHalf; }
-// with a draft tree, behind them: [2][64] visibility words of the rows, [2] nodes
-// that some row sees, [2] nodes with a non-finite value
-constexpr int attn_off_tree(int nr) { return attn_off_p(nr) + 2 * attn_p_buf_bytes(nr); }
-constexpr int kAttnTreeBytes = (2 * 64 + 4) * 8;
-constexpr int attn_smem(int nr, bool tree = false) {
-    return attn_off_tree(nr) + (tree ? kAttnTreeBytes : 0) + 1024;                               // + alignment slack
-}
-static_assert(attn_smem(32, true) <= 227 * 1024 && attn_smem(64, true) <= 227 * 1024, "attention shared memory");
+constexpr int attn_smem(int nr) { return attn_off_p(nr) + 2 * attn_p_buf_bytes(nr) + 1024; }   // + alignment slack
+static_assert(attn_smem(32) <= 227 * 1024 && attn_smem(64) <= 227 * 1024, "attention shared memory");
 
 // mbarriers ([2] = one per ring stage / buffer)
 constexpr int kBarKFull = 0;     // K tile landed (producer expect_tx)
@@ -194,39 +188,13 @@ __device__ __forceinline__ float warp_reduce_scatter16(float (&v)[16], int lane)
     return v[0];
 }
 
-// The draft tree of tree_attn: T nodes a sequence, of which the launch takes
-// the d.Qn query nodes from j0 on.
-struct AttnTree {
-    const uint64_t* mask;      // [B][T] visibility words
-    const uint16_t* v;         // bf16 [B][Hkv][T][128]
-    int T, j0;
-};
-
-// Whether a pair of bf16 holds an infinity or NaN in its low / high half.
-__device__ __forceinline__ bool bf16_lo_wild(uint32_t w) { return (w & 0x00007F80u) == 0x00007F80u; }
-__device__ __forceinline__ bool bf16_hi_wild(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u; }
-
-__device__ __forceinline__ void attn_store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void attn_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void attn_store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void attn_store4(__nv_bfloat16* p, const float4& v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-
-// kTree: one more tile, the last of a unit's last chunk, holds the tree's own
-// keys and values (at most 64 tokens); there a (token, row) pair counts only
-// where the row's visibility word has the token's bit.  A row whose word is 0
-// is empty: its running max is +inf, so all its weights are 0.  A value that
-// is infinite or NaN must not reach the rows that do not see its node (zero
-// times it is NaN), so it enters the product as 0 and the epilogue adds it to
-// the rows that do.
-template <int NR, bool kTree, class OutT>
-__device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q,
-                                          const CUtensorMap& tm_tk, const CUtensorMap& tm_tv, const AttnTree& tr,
-                                          const Dims& d, const int32_t* __restrict__ slot_table,
-                                          const int32_t* __restrict__ ctx_len, float scale_log2, const AttnChunks& ch,
-                                          OutT* __restrict__ out, float* __restrict__ lse_out, float* ws_o,
-                                          float* ws_lse, int* ws_ticket, int* ws_sched) {
+template <int NR>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_q, Dims d, const int32_t* __restrict__ slot_table,
+                       const int32_t* __restrict__ ctx_len, float scale_log2, AttnChunks ch,
+                       float* __restrict__ out, float* __restrict__ lse_out, float* ws_o, float* ws_lse,
+                       int* ws_ticket, int* ws_sched) {
     static_assert(NR == 32 || NR == 64, "rows are padded to 32 or 64");
     constexpr int kPBufs = 2;                                     // P^T buffers
     constexpr int kPBufBytes = attn_p_buf_bytes(NR);
@@ -254,19 +222,11 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
     float* s_fin = reinterpret_cast<float*>(smem + kAttnOffFin);
     float* s_mw = reinterpret_cast<float*>(smem + kAttnOffMw);
     float* s_thr = reinterpret_cast<float*>(smem + kAttnOffThr);
-    uint64_t* s_rowmask = reinterpret_cast<uint64_t*>(smem + attn_off_tree(NR));
-    uint64_t* s_seen = s_rowmask + 2 * 64;
-    uint64_t* s_wild = s_seen + 2;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int K = d.K;
     const int G = d.G();
     const int rows = d.Qn * G;
-    const int q_nodes = kTree ? tr.T : d.Qn;                      // query positions a sequence, and the first one taken
-    const int q_first = kTree ? tr.j0 : 0;
-    auto out_row = [&](int b, int h, int r) {
-        return (static_cast<long long>(b) * q_nodes + q_first + r / G) * d.Hq + h * G + r % G;
-    };
 
     // ---------------------------------------------------------- set-up
     if (tid == 0) {
@@ -343,39 +303,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                 }
             }
             const unsigned m = __ballot_sync(0xFFFFFFFFu, any);
-            int n = __popc(m);
-            if constexpr (kTree) {
-                const uint64_t real = tr.T >= 64 ? ~0ull : (1ull << tr.T) - 1;
-                uint64_t seen = 0;
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int r = 32 * hh + lane;
-                    const uint64_t w = r < rows ? tr.mask[static_cast<long long>(b) * tr.T + tr.j0 + r / G] & real : 0;
-                    s_rowmask[pb * 64 + r] = w;
-                    seen |= w;
-                }
-                const uint32_t lo32 = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(seen));
-                const uint32_t hi32 = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(seen >> 32));
-                seen = lo32 | (static_cast<uint64_t>(hi32) << 32);
-                if (lane == 0) {
-                    s_seen[pb] = seen;
-                    s_wild[pb] = 0;
-                }
-                if (seen == 0) n = 0;                             // every row is empty: nothing is read
-                if (seen != 0 && j == ch.cpu - 1) {
-                    if (lane == 0) {
-                        uint32_t nv = 0;
-#pragma unroll
-                        for (int jj = 0; jj < 4; ++jj)
-                            nv |= static_cast<uint32_t>(min(kBlockTokens, max(0, tr.T - kBlockTokens * jj))) << (8 * jj);
-                        int* e = info + 8 + 4 * n;
-                        e[0] = -1;
-                        e[1] = static_cast<int>(nv);
-                        e[2] = 0;
-                    }
-                    ++n;
-                }
-            }
+            const int n = __popc(m);
             if (any) {
                 int* e = info + 8 + 4 * __popc(m & ((1u << lane) - 1u));
                 e[0] = lo + kAttnTileSlots * lane;
@@ -395,8 +323,8 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                 mbar_arrive_expect_tx(&bar[kBarQFull + pb], static_cast<uint32_t>(rows) * kRowBytes);
                 if (!*s_abort) {
                     uint8_t* q_dst = sQ + (p % kQBufs) * 2 * kAttnQHalf;
-                    tma_load_3d(q_dst, &tm_q, &bar[kBarQFull + pb], 0, h * G, b * q_nodes + q_first, pol_q);
-                    tma_load_3d(q_dst + kAttnQHalf, &tm_q, &bar[kBarQFull + pb], 64, h * G, b * q_nodes + q_first, pol_q);
+                    tma_load_3d(q_dst, &tm_q, &bar[kBarQFull + pb], 0, h * G, b * d.Qn, pol_q);
+                    tma_load_3d(q_dst + kAttnQHalf, &tm_q, &bar[kBarQFull + pb], 64, h * G, b * d.Qn, pol_q);
                 }
             }
             __syncwarp();
@@ -427,18 +355,6 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                     const int st = pos & 1;
                     const int z = zu + info[8 + 4 * i];              // first pool slot of the tile
                     if (pos >= 2) cta_wait(&bar[bar_empty + st], ((pos >> 1) - 1) & 1, s_abort);
-                    if (kTree && info[8 + 4 * i] < 0) {              // the tree's tile: T rows, zeros up to a whole slot
-                        const CUtensorMap* tt = is_k ? &tm_tk : &tm_tv;
-                        const int t16 = (tr.T + kBlockTokens - 1) / kBlockTokens * kBlockTokens;
-                        mbar_arrive_expect_tx(&bar[bar_full + st], static_cast<uint32_t>(t16) * kRowBytes);
-                        if (!*s_abort) {
-                            last[st] = pos;
-                            uint8_t* dst = ring + st * kAttnStageBytes;
-                            tma_load_3d(dst, tt, &bar[bar_full + st], 0, 0, info[2], pol_kv);
-                            tma_load_3d(dst + kAttnHalf, tt, &bar[bar_full + st], 64, 0, info[2], pol_kv);
-                        }
-                        continue;
-                    }
                     mbar_arrive_expect_tx(&bar[bar_full + st], kAttnStageBytes);
                     if (!*s_abort) {
                         last[st] = pos;
@@ -564,8 +480,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
             // probabilities are 0 (the padded columns are never read)
             float* mr = s_m + pb * 64;
             float* thr = s_thr + pb * 64;
-            const uint64_t* rowmask = s_rowmask + pb * 64;
-            if (q == 0 && lane < kH && (r0 + lane >= rows || (kTree && rowmask[r0 + lane] == 0))) {
+            if (q == 0 && lane < kH && r0 + lane >= rows) {
                 const float kPosInf = __int_as_float(0x7f800000);
                 mr[r0 + lane] = thr[r0 + lane] = kPosInf;
             }
@@ -576,8 +491,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                 const int st = pos & 1;
                 const int* e = info + 8 + 4 * i;
                 const int nvj = (static_cast<uint32_t>(myslot < 4 ? e[1] : e[2]) >> (8 * (myslot & 3))) & 0xFF;
-                const bool tree_tile = kTree && e[0] < 0;
-                const bool valid = mytok < nvj && (!tree_tile || (s_seen[pb] >> (tok & 63) & 1));
+                const bool valid = mytok < nvj;
                 cta_wait(&bar[kBarSFull + st], (pos >> 1) & 1, s_abort);
                 __syncwarp();                                 // tcgen05.ld is warp-wide: lanes together
                 tc_fence_after_sync();
@@ -598,24 +512,14 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kBarSFree + st]);
-                if (tree_tile && valid) {
-#pragma unroll
-                    for (int r = 0; r < kH; ++r)
-                        if (!(rowmask[r0 + r] >> tok & 1)) x[r] = kNegInf;
-                }
-                if (tree_tile && i == 0) {
-                    // no token of the cache in this chunk: rows start at -inf, and the vote finds their maxima
-                    if (q == 0 && lane < kH && r0 + lane < rows && rowmask[r0 + lane] != 0)
-                        mr[r0 + lane] = thr[r0 + lane] = kNegInf;
-                    named_bar_sync(nb_sync, kSm);
-                } else if (i == 0) {
+                if (i == 0) {
                     // seed the running max: the first token of the tile's first occupied slot
                     const uint64_t nvs = static_cast<uint32_t>(e[1]) | (static_cast<uint64_t>(static_cast<uint32_t>(e[2])) << 32);
                     const int j0 = (__ffsll(static_cast<long long>(nvs)) - 1) >> 3;
                     if (tok == kBlockTokens * j0) {
 #pragma unroll
                         for (int r = 0; r < kH; ++r)
-                            if (r0 + r < rows && (!kTree || rowmask[r0 + r] != 0)) {
+                            if (r0 + r < rows) {
                                 const float m0 = x[r] * scale_log2;
                                 mr[r0 + r] = m0;
                                 thr[r0 + r] = (m0 + kAttnLazy) * inv_scale;
@@ -756,24 +660,6 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                         }
                     }
                 }
-                if (tree_tile && valid && r0 == 0) {
-                    cta_wait(&bar[kBarVFull + st], (pos >> 1) & 1, s_abort);
-                    uint8_t* vrow = sV + st * kAttnStageBytes + tok * 128;
-                    bool wild = false;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        uint32_t* w = reinterpret_cast<uint32_t*>(vrow + (k & 7) * 16 + (k >> 3) * kAttnHalf);
-                        const uint4 v4 = *reinterpret_cast<const uint4*>(w);
-                        const uint32_t vv[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (bf16_lo_wild(vv[c]) || bf16_hi_wild(vv[c])) {
-                                wild = true;
-                                w[c] = vv[c] & ((bf16_lo_wild(vv[c]) ? 0u : 0xFFFFu) | (bf16_hi_wild(vv[c]) ? 0u : 0xFFFF0000u));
-                            }
-                    }
-                    if (wild) atomicOr(reinterpret_cast<unsigned int*>(s_wild + pb) + (tok >> 5), 1u << (tok & 31));
-                }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -807,7 +693,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
             const int n = info[0], c = info[1], u = info[2], ncu = info[3];
             const bool stop = named_bar_or(kNbEpiVote, 128, n < 0 || *s_abort);
             __syncwarp();
-            if (lane == 0 && (!kTree || stop)) mbar_arrive(&bar[kBarLFree + pb]);
+            if (lane == 0) mbar_arrive(&bar[kBarLFree + pb]);
             if (stop) break;
             cta_wait(&bar[kBarSMDone + pb], (p >> 1) & 1, s_abort);
             cta_wait(&bar[kBarODone + pb], (p >> 1) & 1, s_abort);
@@ -843,24 +729,13 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
 #pragma unroll
                     for (int r = 0; r < 32; ++r) o[r] = 0.f;
                 }
-                if constexpr (kTree) {
-                    // values that are no numbers, to the rows that see their nodes
-                    for (uint64_t w = n > 0 ? s_wild[pb] : 0; w != 0; w &= w - 1) {
-                        const int i = __ffsll(static_cast<long long>(w)) - 1;
-                        const uint32_t bits = static_cast<uint32_t>(tr.v[(static_cast<long long>(u) * tr.T + i) * kHeadDim + chn]) << 16;
-                        if (bf16_hi_wild(bits)) {
-#pragma unroll
-                            for (int r = 0; r < 32; ++r)
-                                if (s_rowmask[pb * 64 + 32 * hh + r] >> i & 1) o[r] += __uint_as_float(bits);
-                        }
-                    }
-                }
 #pragma unroll
                 for (int rr = 0; rr < 32; ++rr) {
                     const int r = 32 * hh + rr;
                     if (r >= rows) break;
                     if (direct) {
-                        attn_store(out + out_row(b, h, r) * kHeadDim + chn, o[rr] * f_inv[r]);
+                        const long long orow = (static_cast<long long>(b) * d.Qn + r / G) * d.Hq + h * G + r % G;
+                        out[orow * kHeadDim + chn] = o[rr] * f_inv[r];
                     } else {
                         dst[r * kHeadDim + chn] = o[rr] * f_inv[r];
                     }
@@ -869,11 +744,11 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
             tc_fence_before_sync();
             named_bar_sync(kNbEpi, 128);                      // every thread has read its O^T
             if (leader) mbar_arrive(&bar[kBarOFree + pb]);
-            if (kTree && lane == 0) mbar_arrive(&bar[kBarLFree + pb]);   // the visibility words are read
             if (direct) {
                 if (q < 2 && 32 * q + lane < rows) {
                     const int r = 32 * q + lane;
-                    lse_out[out_row(b, h, r)] = f_lse[r] * kLn2;
+                    const long long orow = (static_cast<long long>(b) * d.Qn + r / G) * d.Hq + h * G + r % G;
+                    lse_out[orow] = f_lse[r] * kLn2;
                 }
             } else {
                 if (q < 2 && 32 * q + lane < rows) ws_lse[static_cast<long long>(c) * rows + 32 * q + lane] = f_lse[32 * q + lane];
@@ -905,7 +780,8 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                         const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
                         for (int jj = 0; jj < kAttnMaxChunks; ++jj) s_mw[t * kAttnMaxChunks + jj] = lj[jj] * inv;
-                        lse_out[out_row(b, h, t)] = L > 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
+                        const long long orow = (static_cast<long long>(b) * d.Qn + t / G) * d.Hq + h * G + t % G;
+                        lse_out[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
                     }
                     named_bar_sync(kNbEpi, 128);
                     // 32 threads per row (4 channels each), 4 rows per pass: up to 8 float4
@@ -937,7 +813,8 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
                                 acc.z += w[jj] * xv[s2][jj].z;
                                 acc.w += w[jj] * xv[s2][jj].w;
                             }
-                            attn_store4(out + out_row(b, h, r) * kHeadDim + c4, acc);
+                            const long long orow = (static_cast<long long>(b) * d.Qn + r / G) * d.Hq + h * G + r % G;
+                            *reinterpret_cast<float4*>(out + orow * kHeadDim + c4) = acc;
                         }
                     }
                     if (leader) ws_ticket[u] = 0;             // ready for the next call
@@ -959,29 +836,6 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_k, const CUtenso
             atomicExch(ws_sched + 1, 0);
         }
     }
-}
-
-template <int NR>
-__global__ void __launch_bounds__(kAttnThreads, 1)
-    sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ CUtensorMap tm_q, Dims d, const int32_t* __restrict__ slot_table,
-                       const int32_t* __restrict__ ctx_len, float scale_log2, AttnChunks ch,
-                       float* __restrict__ out, float* __restrict__ lse_out, float* ws_o, float* ws_lse,
-                       int* ws_ticket, int* ws_sched) {
-    attn_body<NR, false>(tm_k, tm_v, tm_q, tm_k, tm_v, AttnTree{nullptr, nullptr, 0, 0}, d, slot_table, ctx_len,
-                         scale_log2, ch, out, lse_out, ws_o, ws_lse, ws_ticket, ws_sched);
-}
-
-template <int NR>
-__global__ void __launch_bounds__(kAttnThreads, 1)
-    tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_tk,
-                     const __grid_constant__ CUtensorMap tm_tv, AttnTree tr, Dims d,
-                     const int32_t* __restrict__ slot_table, const int32_t* __restrict__ ctx_len, float scale_log2,
-                     AttnChunks ch, __nv_bfloat16* __restrict__ out, float* __restrict__ lse_out, float* ws_o,
-                     float* ws_lse, int* ws_ticket, int* ws_sched) {
-    attn_body<NR, true>(tm_k, tm_v, tm_q, tm_tk, tm_tv, tr, d, slot_table, ctx_len, scale_log2, ch, out, lse_out, ws_o,
-                        ws_lse, ws_ticket, ws_sched);
 }
 
 }  // namespace oasis

@@ -18,6 +18,7 @@
 #include "oasis.h"
 
 #include "attn.cuh"
+#include "attn_tree.cuh"
 #include "common.cuh"
 #include "fused.cuh"
 #include "overlap.cuh"

@@ -45,11 +45,48 @@ int make_map_tree(CUtensorMap* m, const void* base, unsigned long long units, in
     return OASIS_OK;
 }
 
-// Nodes of one launch: as many as 64 query rows hold.
-Dims tree_dims(const Dims& d, int T) {
-    Dims t = d;
-    t.Qn = std::min(T, 64 / d.G());
-    return t;
+// Work of a tree attention call: items of up to two row tiles (128 query rows
+// each, whole nodes), KV tiles a unit (8 slots each, and the tree's own), and
+// the equal stretch of all items' KV tiles that a CTA takes.  An SM that the
+// gather occupies cannot hold an attention CTA beside it (as in
+// oasis_sparse_attn), so the gather's SMs are left free.
+struct TreeWork {
+    int nt, pairs, tpu, per, total, ctas, grid_max;
+};
+
+TreeWork tree_work(const Dims& d, int T) {
+    TreeWork w;
+    w.nt = std::min(T, oasis::kTaRows / d.G());
+    const int tiles = (T + w.nt - 1) / w.nt;
+    w.pairs = (tiles + 1) / 2;
+    w.tpu = (d.K + oasis::kAttnTileSlots - 1) / oasis::kAttnTileSlots + 1;
+    const long long total = static_cast<long long>(d.B) * d.Hkv * w.pairs * w.tpu;
+    w.total = static_cast<int>(total);           // <= 65535 units x 64 pairs x 129 tiles: below 2^31 (checked by the caller)
+    w.grid_max = std::max(1, sm_count() - oasis::kPrefetchCtas);
+    w.per = static_cast<int>((total + w.grid_max - 1) / w.grid_max);
+    w.per = std::max(w.per, std::min(w.tpu, 2));
+    // whole items where that makes no CTA's share much longer: a split item costs its parts' trip through the
+    // workspace and the joining, about four tiles' time
+    const int whole = (w.per + w.tpu - 1) / w.tpu * w.tpu;
+    if (whole <= w.per + 4) w.per = whole;
+    w.ctas = static_cast<int>((total + w.per - 1) / w.per);
+    return w;
+}
+
+// Workspace: the parts' outputs and log2-sum-exps (two places a CTA), a ticket
+// an item (zero between calls).
+struct TreeWs {
+    size_t o, lse, ticket, total;
+};
+
+TreeWs tree_ws(const Dims& d, const TreeWork& w) {
+    TreeWs s;
+    const size_t rows = static_cast<size_t>(w.grid_max) * 2 * 256;
+    s.o = 0;
+    s.lse = align256(rows * oasis::kHeadDim * sizeof(float));
+    s.ticket = align256(s.lse + rows * sizeof(float));
+    s.total = align256(s.ticket + static_cast<size_t>(d.B) * d.Hkv * w.pairs * sizeof(int));
+    return s;
 }
 
 int check_tree_heads(const Dims& d) {
@@ -116,15 +153,15 @@ int oasis_qk_norm_rope(const oasis_dims* dp, int32_t n_tok, const void* qkv, siz
 size_t oasis_tree_workspace_bytes(const oasis_dims* dp, int32_t n_tree) {
     Dims d;
     if (check_tree(dp, n_tree, &d) != OASIS_OK || check_tree_heads(d) != OASIS_OK) return 0;
-    return ws_layout(tree_dims(d, n_tree)).total;
+    return tree_ws(d, tree_work(d, n_tree)).total;
 }
 
 int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const void* pool, const int32_t* slot_table,
                     const int32_t* ctx_len, const void* k_tree, const void* v_tree, const uint64_t* mask, float scale,
                     void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
-    Dims full;
-    if (int rc = check_tree(dp, n_tree, &full)) return rc;
-    if (int rc = check_tree_heads(full)) return rc;
+    Dims d;
+    if (int rc = check_tree(dp, n_tree, &d)) return rc;
+    if (int rc = check_tree_heads(d)) return rc;
     if (int rc = check_ptr(q, "q")) return rc;
     if (int rc = check_ptr(pool, "pool")) return rc;
     if (int rc = check_ptr(slot_table, "slot_table")) return rc;
@@ -136,9 +173,10 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
     if (int rc = check_ptr(lse, "lse")) return rc;
     if (int rc = check_ptr(ws, "ws")) return rc;
     if (!(scale > 0.f) || !(scale < 3.0e38f)) return fail(OASIS_EINVAL, "scale must be a positive finite float");
-    Dims d = tree_dims(full, n_tree);
-    const WsLayout w = ws_layout(d);
-    if (ws_bytes < w.total) return fail(OASIS_EINVAL, "workspace too small: %zu < %zu", ws_bytes, w.total);
+    const TreeWork w = tree_work(d, n_tree);
+    if (static_cast<long long>(d.B) * d.Hkv * w.pairs * w.tpu > 0x3FFFFFFFll) return fail(OASIS_EINVAL, "too many rows");
+    const TreeWs ly = tree_ws(d, w);
+    if (ws_bytes < ly.total) return fail(OASIS_EINVAL, "workspace too small: %zu < %zu", ws_bytes, ly.total);
     CUtensorMap tk, tv, tq, ttk, ttv;
     const unsigned long long units = static_cast<unsigned long long>(d.B) * d.Hkv;
     if (int rc = make_map_pool(&tk, pool, units * d.K, "pool keys")) return rc;
@@ -146,33 +184,32 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
         return rc;
     if (int rc = make_map_tree(&ttk, k_tree, units, n_tree, "tree keys")) return rc;
     if (int rc = make_map_tree(&ttv, v_tree, units, n_tree, "tree values")) return rc;
+    Dims dq = d;
+    dq.Qn = n_tree;
+    if (int rc = make_map_q(&tq, q, dq, w.nt)) return rc;
+    static OncePerDevice once;
+    if (int rc = once([] { return set_smem(oasis::tree_attn_kernel, oasis::kTaSmem, "tree_attn smem"); })) return rc;
     uint8_t* base = static_cast<uint8_t*>(ws);
-    float* ws_lse = reinterpret_cast<float*>(base + w.lse);
-    float* ws_o = reinterpret_cast<float*>(base + w.o);
-    int* ws_ticket = reinterpret_cast<int*>(base + w.ticket);
-    int* ws_sched = reinterpret_cast<int*>(base + w.sched);
-    const float scale_log2 = scale * 1.4426950408889634f;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int per = d.Qn;
-    for (int j0 = 0; j0 < n_tree; j0 += per) {
-        d.Qn = std::min(per, n_tree - j0);
-        Dims dq = d;
-        dq.Qn = n_tree;
-        if (int rc = make_map_q(&tq, q, dq, d.Qn)) return rc;
-        const oasis::AttnChunks chunks = attn_chunks(d, sm_count());
-        const int grid_max = std::max(1, sm_count() - oasis::kPrefetchCtas);
-        const unsigned ctas = static_cast<unsigned>(std::min(grid_max, chunks.nc));
-        const bool r32 = d.Qn * d.G() <= 32;
-        auto kern = r32 ? oasis::tree_attn_kernel<32> : oasis::tree_attn_kernel<64>;
-        const int smem = oasis::attn_smem(r32 ? 32 : 64, true);
-        static OncePerDevice once[2];
-        if (int rc = once[r32]([&] { return set_smem(kern, smem, "tree_attn smem"); })) return rc;
-        const oasis::AttnTree tr{mask, static_cast<const uint16_t*>(v_tree), n_tree, j0};
-        kern<<<ctas, oasis::kAttnThreads, smem, s>>>(tk, tv, tq, ttk, ttv, tr, d, slot_table, ctx_len, scale_log2, chunks,
-                                                     static_cast<__nv_bfloat16*>(out), lse, ws_o, ws_lse, ws_ticket, ws_sched);
-        if (int rc = check_launch("tree_attn launch")) return rc;
-    }
-    return OASIS_OK;
+    oasis::TreeAttnArgs a;
+    a.slot_table = slot_table;
+    a.ctx_len = ctx_len;
+    a.mask = mask;
+    a.v_tree = static_cast<const uint16_t*>(v_tree);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.ws_o = reinterpret_cast<float*>(base + ly.o);
+    a.ws_lse = reinterpret_cast<float*>(base + ly.lse);
+    a.ticket = reinterpret_cast<int*>(base + ly.ticket);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.T = n_tree;
+    a.nt = w.nt;
+    a.pairs = w.pairs;
+    a.tpu = w.tpu;
+    a.per = w.per;
+    a.total = w.total;
+    oasis::tree_attn_kernel<<<static_cast<unsigned>(w.ctas), oasis::kTaThreads, oasis::kTaSmem,
+                              static_cast<cudaStream_t>(stream)>>>(tk, tv, tq, ttk, ttv, d, a);
+    return check_launch("tree_attn launch");
 }
 
 int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const float* probs, const float* draft_probs,
