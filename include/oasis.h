@@ -382,8 +382,8 @@ int oasis_qk_norm_rope(const oasis_dims* d, int32_t n_tok, const void* qkv, size
                        void* stream);
 
 /* Workspace bytes of oasis_tree_attn (0 for bad dims).  Device memory that
- * must be zero-filled once before its first use; the kernel leaves it ready
- * for the next call.  Calls on one workspace must be stream-ordered. */
+ * needs no preparation and keeps nothing between calls; calls on one workspace
+ * must be stream-ordered. */
 size_t oasis_tree_workspace_bytes(const oasis_dims* d, int32_t n_tree);
 
 /* Attention of a tree's nodes over the resident pool slots (as

@@ -32,7 +32,9 @@
 // equal stretch of it (`per` tiles), so every SM has the same share whatever the
 // number of items.  An item that lies in one stretch is written directly; the
 // parts of others go to the workspace, normalised, with their log2-sum-exp, and
-// the last part's CTA joins them.
+// a second kernel joins them, a warp a row.  (Joined by the item's last CTA
+// instead, 28 rows of 9 parts took 20 us: one SM for each item, all its loads
+// waiting for one another, and code that no SM had fetched yet.)
 //
 // Roles (12 warps, mbarriers for every hand-off, every wait bounded):
 //   warps 0-3, 4-7  softmax of the even / odd steps and the epilogue
@@ -91,7 +93,7 @@ constexpr int kTaStagger = 8;
 constexpr uint32_t kTcS = 0, kTcO = 256;
 
 // Header of a segment's list.
-enum { kTiN = 0, kTiItem, kTiDirect, kTiSlot, kTiParts, kTiFirstCta, kTiSeenLo, kTiSeenHi, kTiWildLo, kTiWildHi };
+enum { kTiN = 0, kTiItem, kTiDirect, kTiSlot, kTiSeenLo, kTiSeenHi, kTiWildLo, kTiWildHi };
 // Flags of a tile (4th int).
 constexpr int kTfMask = 1, kTfClean = 2;
 
@@ -104,7 +106,6 @@ struct TreeAttnArgs {
     float* lse;                  // [B][T][Hq]
     float* ws_o;                 // [2 CTAs][256][128]
     float* ws_lse;               // [2 CTAs][256]
-    int* ticket;                 // [items]
     float scale_log2;
     int T;
     int nt;                      // nodes a row tile
@@ -214,7 +215,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     int* misc = reinterpret_cast<int*>(smem + kTaOffMisc);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc);
     volatile int* s_abort = misc + 1;
-    volatile int* s_last = misc + 2;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = d.G(), K = d.K;
@@ -307,8 +307,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             info[kTiDirect] = c0 == c1;
             // a CTA's first segment goes to its first place in the workspace, its last to its second
             info[kTiSlot] = 2 * static_cast<int>(blockIdx.x) + (p == 0 ? 0 : 1);
-            info[kTiParts] = c1 - c0 + 1;
-            info[kTiFirstCta] = c0;
             info[kTiSeenLo] = static_cast<int>(static_cast<uint32_t>(seen));
             info[kTiSeenHi] = static_cast<int>(static_cast<uint32_t>(seen >> 32));
             info[kTiWildLo] = info[kTiWildHi] = 0;
@@ -330,7 +328,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             mbar_init(&bar[i], cnt);
         }
         fence_mbar_init();
-        *s_last = 0;
     }
     if (warp == kTaLister) {
         if (lane == 0) *s_abort = 0;
@@ -762,8 +759,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int prow = (sq.two ? wg : 0) * 128 + r;         // row of the item
             const int orow = !live0 ? -1
                              : direct ? (b * a.T + j) * d.Hq + h * G + r % G : info[kTiSlot] * 256 + prow;
-            char* const dst = direct ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.ws_o);
-            const int pitch = direct ? kHeadDim * 2 : kHeadDim * 4;
             uint4* const stage = reinterpret_cast<uint4*>(smem + kTaOffStage + warp * 32 * kTaStagePitch);
             // 32 channels at a time; with one row tile the warpgroups take 64 channels each, with two a row tile each
             const int c_lo = sq.two ? 0 : 2 * wg, c_hi = sq.two ? 4 : 2 * wg + 2;
@@ -795,34 +790,34 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 }
-                // 64 B of each row at a time through the warp's staging rows, so that four lanes write a row's 64 B
+                if (!direct) {
+                    float4* to = reinterpret_cast<float4*>(a.ws_o + static_cast<long long>(orow) * kHeadDim + 32 * c);
+                    if (live0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                    continue;
+                }
+                // through the warp's staging rows, so that four lanes write a row's 64 B
                 uint4* const own = stage + lane * (kTaStagePitch / 16);
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    if (direct && hh == 1) break;
-                    if (direct) {
+                for (int i = 0; i < 4; ++i)
+                    own[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                        pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                __syncwarp();
+                uint4 v[4];
+                int row[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            own[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            own[i] = make_uint4(__float_as_uint(o[16 * hh + 4 * i]), __float_as_uint(o[16 * hh + 4 * i + 1]),
-                                                __float_as_uint(o[16 * hh + 4 * i + 2]), __float_as_uint(o[16 * hh + 4 * i + 3]));
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int from = 8 * i + (lane >> 2);
-                        const int row = __shfl_sync(0xFFFFFFFFu, orow, from);
-                        const uint4 v = stage[from * (kTaStagePitch / 16) + (lane & 3)];
-                        if (row >= 0)
-                            *reinterpret_cast<uint4*>(dst + static_cast<long long>(row) * pitch +
-                                                      (direct ? 64 * c : 128 * c + 64 * hh) + 16 * (lane & 3)) = v;
-                    }
-                    __syncwarp();
+                for (int i = 0; i < 4; ++i) {
+                    const int from = 8 * i + (lane >> 2);
+                    row[i] = __shfl_sync(0xFFFFFFFFu, orow, from);
+                    v[i] = stage[from * (kTaStagePitch / 16) + (lane & 3)];
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row[i] >= 0)
+                        *reinterpret_cast<uint4*>(a.out + static_cast<long long>(row[i]) * kHeadDim + 32 * c + 8 * (lane & 3)) = v[i];
+                __syncwarp();
             }
             if (live0 && (sq.two || wg == 0)) {
                 if (direct)
@@ -833,84 +828,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0 && n > 0) mbar_arrive(&bar[kTbOFree]);
-            if (!direct) {
-                const int parts = info[kTiParts], c0 = info[kTiFirstCta];
-                __threadfence();
-                named_bar_sync(kTnSync, 256);
-                if (tid == 0) *s_last = atomicAdd(a.ticket + item, 1) == parts - 1 ? 1 : 0;
-                named_bar_sync(kTnSync, 256);
-                if (*s_last) {
-                    // join the item's parts: out = sum_j 2^(lse_j - M) o_j / sum_j 2^(lse_j - M).  Thread `tid`
-                    // reduces row tid's log2-sum-exps to M and 1 / sum; then a warp takes four rows at a time, a
-                    // float4 a lane, with the loads of the rows and parts in flight together.
-                    __threadfence();
-                    auto place = [&](int k) {
-                        const int c = c0 + k;
-                        return 2 * c + (static_cast<int>(static_cast<long long>(c) * a.per / a.tpu) == item ? 0 : 1);
-                    };
-                    auto node_of = [&](int row) { return (2 * pr + (row >> 7)) * a.nt + (row & 127) / G; };
-                    auto row_of = [&](int row) {
-                        return (static_cast<long long>(b) * a.T + node_of(row)) * d.Hq + h * G + (row & 127) % G;
-                    };
-                    auto is_row = [&](int row) { return (row & 127) < a.nt * G && node_of(row) < a.T; };
-                    {
-                        float M = kNegInf, L = 0.f;
-                        if (is_row(tid)) {
-#pragma unroll 8
-                            for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(a.ws_lse + place(k) * 256ll + tid));
-#pragma unroll 8
-                            for (int k = 0; k < parts; ++k) {
-                                const float lk = __ldcg(a.ws_lse + place(k) * 256ll + tid);
-                                L += lk == kNegInf ? 0.f : exp2f(lk - M);   // an empty part: 0
-                            }
-                            a.lse[row_of(tid)] = L != 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
-                        }
-                        s_m[tid] = M;
-                        s_l[tid] = L != 0.f ? 1.f / L : 0.f;
-                    }
-                    named_bar_sync(kTnSync, 256);
-                    for (int row0 = 4 * warp; row0 < 256; row0 += 32) {
-                        if (!is_row(row0) && !is_row(row0 + 3)) continue;
-                        float4 acc[4];
-                        float M[4], inv[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            M[i] = s_m[row0 + i];
-                            inv[i] = s_l[row0 + i];
-                        }
-#pragma unroll 4
-                        for (int k = 0; k < parts; ++k) {
-                            const long long at = place(k) * 256ll + row0;
-                            float4 v[4];
-                            float lk[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const bool on = is_row(row0 + i);
-                                lk[i] = on ? __ldcg(a.ws_lse + at + i) : kNegInf;
-                                v[i] = on ? __ldcg(reinterpret_cast<const float4*>(a.ws_o + (at + i) * kHeadDim) + lane)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (lk[i] == kNegInf) continue;
-                                const float w = exp2f(lk[i] - M[i]) * inv[i];
-                                acc[i].x += w * v[i].x;
-                                acc[i].y += w * v[i].y;
-                                acc[i].z += w * v[i].z;
-                                acc[i].w += w * v[i].w;
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (is_row(row0 + i))
-                                reinterpret_cast<uint2*>(a.out + row_of(row0 + i) * kHeadDim)[lane] =
-                                    make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w));
-                    }
-                    if (tid == 0) a.ticket[item] = 0;             // ready for the next call
-                }
-                named_bar_sync(kTnSync, 256);                     // s_last may be rewritten
-            }
             if (lane == 0) mbar_arrive(&bar[kTbLFree + pb]);
         }
     }
@@ -920,6 +837,58 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     if (warp == kTaMma) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the rows of split items: out = sum_k 2^(lse_k - M) o_k /
+// sum_k 2^(lse_k - M).  A warp a row, a part a lane for the weights, then a
+// float4 a lane for the channels.
+constexpr int kTjWarps = 4;
+__global__ void __launch_bounds__(32 * kTjWarps) tree_join_kernel(const Dims d, const TreeAttnArgs a) {
+    const float kNegInf = -__int_as_float(0x7f800000);
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kTjWarps + (threadIdx.x >> 5);   // (b, node, head)
+    if (row >= d.B * a.T * d.Hq) return;
+    const int G = d.G();
+    const int hq = row % d.Hq, bj = row / d.Hq;
+    const int j = bj % a.T, b = bj / a.T;
+    const int h = hq / G, tile = j / a.nt;
+    const int item = (b * d.Hkv + h) * a.pairs + (tile >> 1);
+    const int base = item * a.tpu;
+    const int c0 = base / a.per, parts = (base + a.tpu - 1) / a.per - c0 + 1;
+    if (parts == 1) return;                                       // written directly
+    const long long prow = (tile & 1) * 128 + (j - tile * a.nt) * G + hq - h * G;
+    // the item is the last segment of its first CTA, and the first one of the others
+    const long long place0 = 2 * c0 + (c0 * a.per / a.tpu == item ? 0 : 1);
+    auto at = [&](int k) { return (k == 0 ? place0 : 2ll * (c0 + k)) * 256 + prow; };
+    float M = kNegInf, L = 0.f;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        const float lk = k0 + lane < parts ? a.ws_lse[at(k0 + lane)] : kNegInf;
+        const float m = fmaxf(M, warp_max_f32(lk));
+        L = m != kNegInf ? L * exp2f(M - m) : L;
+        L += lk == kNegInf ? 0.f : exp2f(lk - m);                 // an empty part: 0
+        M = m;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        const float lk = k0 + lane < parts ? a.ws_lse[at(k0 + lane)] : kNegInf;
+        const float w = lk == kNegInf ? 0.f : exp2f(lk - M) * inv;
+        const int nk = min(32, parts - k0);
+#pragma unroll 8
+        for (int k = 0; k < nk; ++k) {
+            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+            const float4 v = reinterpret_cast<const float4*>(a.ws_o + at(k0 + k) * kHeadDim)[lane];
+            acc.x += wk * v.x;
+            acc.y += wk * v.y;
+            acc.z += wk * v.z;
+            acc.w += wk * v.w;
+        }
+    }
+    reinterpret_cast<uint2*>(a.out + static_cast<long long>(row) * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    if (lane == 0) a.lse[row] = L != 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
 }
 
 }  // namespace oasis

@@ -73,10 +73,9 @@ TreeWork tree_work(const Dims& d, int T) {
     return w;
 }
 
-// Workspace: the parts' outputs and log2-sum-exps (two places a CTA), a ticket
-// an item (zero between calls).
+// Workspace: the parts' outputs and log2-sum-exps, two places a CTA.
 struct TreeWs {
-    size_t o, lse, ticket, total;
+    size_t o, lse, total;
 };
 
 TreeWs tree_ws(const Dims& d, const TreeWork& w) {
@@ -84,8 +83,7 @@ TreeWs tree_ws(const Dims& d, const TreeWork& w) {
     const size_t rows = static_cast<size_t>(w.grid_max) * 2 * 256;
     s.o = 0;
     s.lse = align256(rows * oasis::kHeadDim * sizeof(float));
-    s.ticket = align256(s.lse + rows * sizeof(float));
-    s.total = align256(s.ticket + static_cast<size_t>(d.B) * d.Hkv * w.pairs * sizeof(int));
+    s.total = align256(s.lse + rows * sizeof(float));
     return s;
 }
 
@@ -188,7 +186,11 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
     dq.Qn = n_tree;
     if (int rc = make_map_q(&tq, q, dq, w.nt)) return rc;
     static OncePerDevice once;
-    if (int rc = once([] { return set_smem(oasis::tree_attn_kernel, oasis::kTaSmem, "tree_attn smem"); })) return rc;
+    if (int rc = once([] {
+            if (int rc = carveout(oasis::tree_join_kernel, "tree_join carve-out")) return rc;
+            return set_smem(oasis::tree_attn_kernel, oasis::kTaSmem, "tree_attn smem");
+        }))
+        return rc;
     uint8_t* base = static_cast<uint8_t*>(ws);
     oasis::TreeAttnArgs a;
     a.slot_table = slot_table;
@@ -199,7 +201,6 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
     a.lse = lse;
     a.ws_o = reinterpret_cast<float*>(base + ly.o);
     a.ws_lse = reinterpret_cast<float*>(base + ly.lse);
-    a.ticket = reinterpret_cast<int*>(base + ly.ticket);
     a.scale_log2 = scale * 1.4426950408889634f;
     a.T = n_tree;
     a.nt = w.nt;
@@ -209,7 +210,12 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
     a.total = w.total;
     oasis::tree_attn_kernel<<<static_cast<unsigned>(w.ctas), oasis::kTaThreads, oasis::kTaSmem,
                               static_cast<cudaStream_t>(stream)>>>(tk, tv, tq, ttk, ttv, d, a);
-    return check_launch("tree_attn launch");
+    if (int rc = check_launch("tree_attn launch")) return rc;
+    if (w.per % w.tpu == 0) return OASIS_OK;     // whole items
+    const unsigned rows = static_cast<unsigned>(d.B) * n_tree * d.Hq;
+    oasis::tree_join_kernel<<<(rows + oasis::kTjWarps - 1) / oasis::kTjWarps, 32 * oasis::kTjWarps, 0,
+                              static_cast<cudaStream_t>(stream)>>>(d, a);
+    return check_launch("tree_join launch");
 }
 
 int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const float* probs, const float* draft_probs,

@@ -148,7 +148,7 @@ def tree_workspace_bytes(d: Dims, n_tree) -> int:
 
 
 def tree_attn(d: Dims, n_tree, q, pool, slot_table, ctx_len, k_tree, v_tree, mask, scale, out, lse, ws, stream=None):
-    """out: bf16 [B, T, Hq, 128], lse: fp32 [B, T, Hq]; ws: a zero-filled tensor of tree_workspace_bytes(d, n_tree)."""
+    """out: bf16 [B, T, Hq, 128], lse: fp32 [B, T, Hq]; ws: any tensor of tree_workspace_bytes(d, n_tree) bytes."""
     w = "oasis_tree_attn"
     dev = _device()
     n = _tree(d, n_tree, w)
