@@ -224,7 +224,8 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
                       int32_t* next_token, void* stream) {
     Dims d;
     if (int rc = check_tree(dp, n_tree, &d)) return rc;
-    if (vocab < 1 || vocab > (1 << 30)) return fail(OASIS_EINVAL, "vocab must be in [1, 2^30] (got %d)", vocab);
+    if (vocab < 1 || vocab > oasis::kVerMaxVocab)
+        return fail(OASIS_EINVAL, "vocab must be in [1, %d] (got %d)", oasis::kVerMaxVocab, vocab);
     if (row_stride < static_cast<size_t>(vocab) || row_stride > (size_t(1) << 40))
         return fail(OASIS_EINVAL, "row_stride must be >= vocab (got %zu)", row_stride);
     if (int rc = check_ptr(probs, "probs")) return rc;
@@ -238,7 +239,14 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
     if (int rc = check_ptr(n_accept, "n_accept")) return rc;
     if (int rc = check_ptr(next_token, "next_token")) return rc;
     static OncePerDevice once;
-    if (int rc = once([] { return carveout(oasis::verify_tree_kernel, "verify_tree carve-out"); })) return rc;
+    if (int rc = once([] {
+            const int most = 2 * 16 * oasis::ver_cap(oasis::kVerMaxVocab, oasis::kVerMaxCluster);
+            if (int rc = set_smem(oasis::verify_tree_kernel, most, "verify_tree smem")) return rc;
+            const cudaError_t e =
+                cudaFuncSetAttribute(oasis::verify_tree_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            return e == cudaSuccess ? OASIS_OK : cuda_fail(e, "verify_tree cluster size");
+        }))
+        return rc;
     oasis::VerifyArgs a;
     a.probs = probs;
     a.draft = draft_probs;
@@ -254,8 +262,25 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
     a.B = d.B;
     a.T = n_tree;
     a.vocab = vocab;
-    oasis::verify_tree_kernel<<<static_cast<unsigned>(d.B) * oasis::kVerCluster, oasis::kVerThreads, 0,
-                                static_cast<cudaStream_t>(stream)>>>(a);
+    // 16 CTAs a sequence where the rows are long: their shares of two rows then leave room for two CTAs an SM
+    const int cluster = vocab > 65536 ? 16 : 8;
+    const size_t smem = static_cast<size_t>(draft_probs != nullptr ? 2 : 1) * 16 * oasis::ver_cap(vocab, cluster);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(d.B) * cluster);
+    cfg.blockDim = dim3(oasis::kVerThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, oasis::verify_tree_kernel, a);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "verify_tree launch");
+    }
     return check_launch("verify_tree launch");
 }
 
