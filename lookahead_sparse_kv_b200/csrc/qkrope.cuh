@@ -31,11 +31,11 @@ __device__ __forceinline__ uint4 f32x8_round_bf16(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(
+__global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(
     Dims d, int T, int split, const uint16_t* __restrict__ qkv, long long row_stride, const uint16_t* __restrict__ wq,
     const uint16_t* __restrict__ wk, float eps, const float* __restrict__ inv_freq, const int32_t* __restrict__ pos,
     uint16_t* __restrict__ q, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-    __shared__ float2 s_cs[kRopeWarps][64];
+    __shared__ float4 s_cos[kRopeWarps][16], s_sin[kRopeWarps][16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long tokens = static_cast<long long>(d.B) * T;
     const long long w = static_cast<long long>(blockIdx.x) * kRopeWarps + warp;
@@ -56,17 +56,12 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(
             turns -= 2.0 * rint(0.5 * turns);
             float sn, cs;
             sincospif(static_cast<float>(turns), &sn, &cs);
-            s_cs[warp][c] = make_float2(cs, sn);
+            reinterpret_cast<float*>(s_cos[warp])[c] = cs;
+            reinterpret_cast<float*>(s_sin[warp])[c] = sn;
         }
     }
     __syncwarp();
-    float cs[8], sn[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 a = s_cs[warp][8 * sub + i];
-        cs[i] = a.x;
-        sn[i] = a.y;
-    }
+    const bool norm = wq != nullptr || wk != nullptr;
     const uint16_t* row = qkv + tok * row_stride;
     for (int s = part * per; s < min(steps, (part + 1) * per); ++s) {
         const int hd = kRopeStep * s + hl;
@@ -82,10 +77,12 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(
         bf16x8_to_f32(c4, hi);
         const uint16_t* wt = is_q ? wq : wk;
         float ss = 0.f;
+        if (norm) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
+            for (int i = 0; i < 8; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        }
         if (on && !is_v) {
             if (wt != nullptr) {
                 const float r = rsqrtf(ss * (1.f / kHeadDim) + eps);
@@ -99,10 +96,15 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = lo[i], y = hi[i];
-                lo[i] = x * cs[i] - y * sn[i];
-                hi[i] = y * cs[i] + x * sn[i];
+            for (int k4 = 0; k4 < 2; ++k4) {
+                const float4 c = s_cos[warp][2 * sub + k4], n = s_sin[warp][2 * sub + k4];
+                const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = lo[4 * k4 + i], y = hi[4 * k4 + i];
+                    lo[4 * k4 + i] = x * cs[i] - y * sn[i];
+                    hi[4 * k4 + i] = y * cs[i] + x * sn[i];
+                }
             }
             a4 = f32x8_round_bf16(lo);
             c4 = f32x8_round_bf16(hi);
