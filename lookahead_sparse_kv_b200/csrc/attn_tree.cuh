@@ -17,8 +17,10 @@
 // of the last 128 hold whatever they hold.
 //
 // Two softmax warpgroups keep the tensor core and the exponentials busy at
-// once: step s of a segment belongs to warpgroup s & 1, and S of step s + 2 is
-// issued right behind the product of step s.  With two row tiles (an item's
+// once: step s of a segment belongs to warpgroup s & 1.  Its 128 tokens go in two
+// halves: while the second half's weights are made, the first half's product and
+// S of the first half of step s + 2 run (whole steps left each warpgroup waiting
+// for its own two MMAs, 3,650 cycles a KV tile of two row tiles).  With two row tiles (an item's
 // 256 rows) steps 2i and 2i + 1 are the two row tiles on KV tile i, so a KV tile
 // is read once for both; with one row tile (128 rows or fewer) they are KV tiles
 // 2i and 2i + 1, each warpgroup with its own O, joined at the end.
@@ -75,19 +77,14 @@ static_assert(kTaOffBar % 8 == 0 && kTaOffMl % 16 == 0 && kTaOffStage % 16 == 0,
 
 // mbarriers
 constexpr int kTbKFull = 0, kTbKEmpty = 2, kTbVFull = 4, kTbVEmpty = 6, kTbVClean = 8;   // [2] by ring stage
-constexpr int kTbSFull = 10, kTbPFull = 12, kTbPvDone = 14;                              // [2] by warpgroup
-constexpr int kTbLFull = 16, kTbLFree = 18;                                              // [2] by list buffer
-constexpr int kTbQFull = 20, kTbQFree = 21, kTbOFree = 22, kTbFinal = 23;                // (kTbFinal: [2] by issuer)
-constexpr int kTbStagger = 25;
+constexpr int kTbSFull = 10, kTbPFull = 14, kTbPvDone = 18, kTbPvA = 20;                  // by warpgroup (and half: [2][2])
+constexpr int kTbLFull = 22, kTbLFree = 24;                                              // [2] by list buffer
+constexpr int kTbQFull = 26, kTbQFree = 27, kTbOFree = 28, kTbFinal = 29;                // (kTbFinal: [2] by issuer)
 constexpr int kTaLFreeCount = 8 + 3 + 2 + 1;                       // softmax warps, loader lanes, issuers, cleaner
 constexpr uint32_t kTnVote = 1, kTnSync = 2;                       // named barriers of the softmax warps
 
 // Every kTaPolyEvery-th pair of weights is made on the multiply-add pipes.
 constexpr int kTaPolyEvery = 4;
-// Segments of this many steps and more start the second warpgroup behind the
-// first one's first softmax: the two then take turns on the exponentials, each
-// one's MMAs behind the other's softmax (in step, both wait for both's MMAs).
-constexpr int kTaStagger = 8;
 
 // TMEM columns: S (and P over it) of the two warpgroups, then their O
 constexpr uint32_t kTcS = 0, kTcO = 256;
@@ -300,9 +297,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kTaNumBars; ++i) {
             int cnt = 1;
-            if (i == kTbPFull || i == kTbPFull + 1) cnt = 4;
+            if (i >= kTbPFull && i < kTbPFull + 4) cnt = 4;
             if (i == kTbOFree) cnt = 8;
-            if (i == kTbStagger) cnt = 4;
             // a tile, and the query rows, are done with when both issuers say so
             if (i == kTbKEmpty || i == kTbKEmpty + 1 || i == kTbVEmpty || i == kTbVEmpty + 1 || i == kTbQFree) cnt = 2;
             if (i == kTbLFree || i == kTbLFree + 1) cnt = kTaLFreeCount;
@@ -469,15 +465,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         // there its product and the next S go out at once.  The warps stay converged and one elected lane
         // issues: descriptors and addresses then live in uniform registers (a single-lane branch took 150
         // cycles an MMA to issue, over twice the MMA's own time; one warp for both warpgroups 2,250 cycles a
-        // step).  A commit covers everything issued before it, so S of step s + 2 seen means O of step s is done.
-        constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTaRows, kAttnTileTokens);
+        // step).
+        constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTaRows, kAttnTileTokens / 2);
         constexpr uint32_t idesc_o = umma_idesc_bf16_f32_bmn(kTaRows, kHeadDim);
         const int wg = warp - kTaMma;
         const uint64_t k_desc = umma_desc_sw128_lbo_sbo(smem_addr(sK), 16, 1024);
         const uint64_t v_desc = umma_desc_sw128_lbo_sbo(smem_addr(sV), kAttnHalf, 1024);
         const uint32_t t_s = tmem + kTcS + wg * 128, t_o = tmem + kTcO + wg * 128;
         int pos = 0, nz = 0, done = 0;                            // KV tiles, segments (with tiles) and own steps behind
-        int staggered = 0;
         for (int p = 0;; ++p) {
             const int pb = p & 1;
             const bool got = ta_wait(&bar[kTbLFull + pb], (p >> 1) & 1, s_abort);
@@ -494,13 +489,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     const int kt = pos + sq.tile(s);
                     return ta_wait(&bar[kTbKFull + (kt & 1)], (kt >> 1) & 1, s_abort);
                 };
-                // (by the elected lane)
-                auto issue_s = [&](int s) {
-                    const uint64_t ka = k_desc + ((pos + sq.tile(s)) & 1) * (kAttnStageBytes >> 4);
+                // S of 64 tokens of step s (by the elected lane)
+                auto issue_s = [&](int s, int half) {
+                    const uint64_t ka = k_desc + (((pos + sq.tile(s)) & 1) * kAttnStageBytes + half * (kAttnHalf / 2) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const int off = ((ks >> 2) * kAttnHalf + (ks & 3) * 32) >> 4;
-                        umma_bf16(t_s, q_desc + off, ka + off, idesc_s, ks > 0 ? 1u : 0u);
+                        umma_bf16(t_s + 64 * half, q_desc + off, ka + off, idesc_s, ks > 0 ? 1u : 0u);
                     }
                 };
                 // with one row tile a KV tile has one user, who says both words
@@ -509,62 +504,65 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     if (!sq.two) umma_commit(b);
                 };
                 ta_wait(&bar[kTbQFull], nz & 1, s_abort);
-                if (wg == 1 && sq.count() >= kTaStagger) {
-                    ta_wait(&bar[kTbStagger], staggered & 1, s_abort);
-                    ++staggered;
-                }
                 if (mine > 0) {
                     const bool ok = __shfl_sync(0xFFFFFFFFu, wait_k(wg), 0);
                     tc_fence_after_sync();
                     if (elect_one()) {
-                        if (ok) issue_s(wg);
-                        umma_commit(&bar[kTbSFull + wg]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (ok) issue_s(wg, half);
+                            umma_commit(&bar[kTbSFull + 2 * wg + half]);
+                        }
                         release(&bar[kTbKEmpty + ((pos + sq.tile(wg)) & 1)]);
                     }
                     __syncwarp();
                 }
                 if (mine < 2 && elect_one()) umma_commit(&bar[kTbQFree]);
                 if (nz > 0) ta_wait(&bar[kTbOFree], (nz - 1) & 1, s_abort);   // the last segment's O is read
+                uint32_t acc = 0u;                                // the first product overwrites O
                 for (int k = 0; k < mine; ++k, ++done) {
                     const int s = 2 * k + wg, i = sq.tile(s), vt = pos + i, st = vt & 1;
                     const bool more = k + 1 < mine;
-                    const uint32_t nvlo = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(info[16 + 4 * i + 1]), 0);
-                    const uint32_t nvhi = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(info[16 + 4 * i + 2]), 0);
-                    // no byte is 0: every slot counts
-                    const bool full = !((nvlo - 0x01010101u) & ~nvlo & 0x80808080u) && !((nvhi - 0x01010101u) & ~nvhi & 0x80808080u);
                     bool ok = ta_wait(&bar[kTbVClean + st], (vt >> 1) & 1, s_abort);
                     if (more) ok = wait_k(s + 2) && ok;
-                    ok = ta_wait(&bar[kTbPFull + wg], done & 1, s_abort) && ok;
-                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                    tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint64_t va = v_desc + st * (kAttnStageBytes >> 4);
-                        constexpr int kSlot = kBlockTokens * 128 >> 4;
-                        uint32_t acc = k > 0 ? 1u : 0u;           // the first product overwrites O
-                        if (ok && full) {
 #pragma unroll
-                            for (int kk = 0; kk < kAttnTileSlots; ++kk)
-                                umma_bf16_ts(t_o, t_s + 8 * kk, va + kk * kSlot, idesc_o, kk > 0 ? 1u : acc);
-                        } else if (ok) {
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t nv = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(info[16 + 4 * i + 1 + half]), 0);
+                        ok = ta_wait(&bar[kTbPFull + 2 * wg + half], done & 1, s_abort) && ok;
+                        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint64_t va = v_desc + (st * kAttnStageBytes + half * 4 * kBlockTokens * 128 >> 4);
+                            const uint32_t pa = t_s + 64 * half;
+                            constexpr int kSlot = kBlockTokens * 128 >> 4;
+                            if (ok && !((nv - 0x01010101u) & ~nv & 0x80808080u)) {   // no byte is 0: every slot counts
 #pragma unroll
-                            for (int kk = 0; kk < kAttnTileSlots; ++kk) {
-                                if (((kk < 4 ? nvlo : nvhi) >> (8 * (kk & 3)) & 0xFFu) == 0) continue;   // free: no product
-                                umma_bf16_ts(t_o, t_s + 8 * kk, va + kk * kSlot, idesc_o, acc);
-                                acc = 1u;
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16_ts(t_o, pa + 8 * kk, va + kk * kSlot, idesc_o, kk > 0 ? 1u : acc);
+                            } else if (ok) {
+                                uint32_t on = acc;
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    if ((nv >> (8 * kk) & 0xFFu) == 0) continue;     // free: no product
+                                    umma_bf16_ts(t_o, pa + 8 * kk, va + kk * kSlot, idesc_o, on);
+                                    on = 1u;
+                                }
+                            }
+                            if (half == 0) umma_commit(&bar[kTbPvA + wg]);
+                            if (more) {
+                                if (ok) issue_s(s + 2, half);     // behind the product that reads P over this S
+                                umma_commit(&bar[kTbSFull + 2 * wg + half]);
+                            }
+                            if (half == 1) {
+                                if (!more) umma_commit(&bar[kTbPvDone + wg]);
+                                release(&bar[kTbVEmpty + st]);
+                                if (more) release(&bar[kTbKEmpty + ((pos + sq.tile(s + 2)) & 1)]);
+                                if (k + 2 == mine) umma_commit(&bar[kTbQFree]);
                             }
                         }
-                        if (more) {
-                            if (ok) issue_s(s + 2);               // behind the product that reads P over this S
-                            umma_commit(&bar[kTbSFull + wg]);
-                            release(&bar[kTbVEmpty + st]);
-                            release(&bar[kTbKEmpty + ((pos + sq.tile(s + 2)) & 1)]);
-                            if (k + 2 == mine) umma_commit(&bar[kTbQFree]);
-                        } else {
-                            umma_commit(&bar[kTbPvDone + wg]);
-                            release(&bar[kTbVEmpty + st]);
-                        }
+                        acc |= nv != 0 ? 1u : 0u;
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 pos += n;
                 ++nz;
@@ -604,99 +602,108 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const bool live = word != 0;
             const bool warp_live = __any_sync(0xFFFFFFFFu, live);
             float m = kNegInf, l = 0.f;                           // running max (log2 units) and sum
+            bool begun = false;
             const int mine = sq.count_of(wg);
-            for (int k = 0; k < mine; ++k) {
+            for (int k = 0; k < mine; ++k, ++done) {
                 const int* e = info + 16 + 4 * sq.tile(2 * k + wg);
-                ta_wait(&bar[kTbSFull + wg], done & 1, s_abort);
-                __syncwarp();
-                tc_fence_after_sync();
-                if (warp_live) {
-                    uint32_t x[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, x[c]);
-                    tmem_ld_wait();
-                    if (e[3] & kTfMask) {
-                        if (e[0] < 0) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t w = c == 0 ? static_cast<uint32_t>(word) : c == 1 ? static_cast<uint32_t>(word >> 32) : 0u;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!(w >> i & 1)) x[c][i] = 0xFF800000u;
-                            }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t nv = static_cast<uint32_t>(c < 2 ? e[1] : e[2]) >> (16 * (c & 1));
-                                const int n0 = nv & 0xFF, n1 = (nv >> 8) & 0xFF;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if ((i & 15) >= (i < 16 ? n0 : n1)) x[c][i] = 0xFF800000u;
-                            }
-                        }
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        mx[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-                        for (int i = 2; i < 32; i += 2)
-                            mx[c] = max3_nan(mx[c], __uint_as_float(x[c][i - 1]), __uint_as_float(x[c][i]));
-                    }
-                    float top = max3_nan(max3_nan(mx[0], mx[1], __uint_as_float(x[0][31])),
-                                         max3_nan(mx[2], mx[3], __uint_as_float(x[1][31])),
-                                         max3_nan(__uint_as_float(x[2][31]), __uint_as_float(x[3][31]), kNegInf)) *
-                                a.scale_log2;
-                    if (!(top < __int_as_float(0x7f800000))) top = __int_as_float(0x7fc00000);   // an infinite score: NaN
-                    if (k == 0) {
-                        m = top;
-                    } else {
-                        // the running max moves only when a tile exceeds it by more than 2^32 (this S seen: the
-                        // last step's product has landed in O)
-                        const bool up = live && !(top <= m + kAttnLazy);
-                        if (__any_sync(0xFFFFFFFFu, up)) {
-                            const float alpha = up ? attn_exp2(m - top) : 1.f;
-                            if (up) m = top;
-                            l *= alpha;
 #pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t o[16];
-                                tmem_ld_x16(t_o + wg * 128 + 16 * c, o);
-                                tmem_ld_wait();
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t nv = static_cast<uint32_t>(e[1 + half]);
+                    const uint32_t t_x = t_s + 64 * half;
+                    ta_wait(&bar[kTbSFull + 2 * wg + half], done & 1, s_abort);
+                    __syncwarp();
+                    tc_fence_after_sync();
+                    if (warp_live && nv != 0) {
+                        uint32_t x[2][32];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                                tmem_st_x16(t_o + wg * 128 + 16 * c, o);
+                        for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(t_x + 32 * c, x[c]);
+                        tmem_ld_wait();
+                        if (e[3] & kTfMask) {
+                            if (e[0] < 0) {
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const uint32_t w = static_cast<uint32_t>(word >> (32 * c));
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (!(w >> i & 1)) x[c][i] = 0xFF800000u;
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const int n0 = nv >> (16 * c) & 0xFF, n1 = nv >> (16 * c + 8) & 0xFF;
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if ((i & 15) >= (i < 16 ? n0 : n1)) x[c][i] = 0xFF800000u;
+                                }
                             }
-                            tmem_st_wait();
                         }
-                    }
-                    const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2), m2 = f32x2(-m, -m);
-                    uint64_t sum2 = 0ull;
+                        float mx[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t* y = x[c >> 1] + 16 * (c & 1);
+                            mx[c] = __uint_as_float(y[0]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint64_t y =
-                                fma_f32x2(f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, m2);
-                            const uint64_t p2 = i % kTaPolyEvery == kTaPolyEvery - 1
-                                                    ? exp2_poly_f32x2(y)
-                                                    : f32x2(attn_exp2(f32x2_lo(y)), attn_exp2(f32x2_hi(y)));
-                            sum2 = add_f32x2(sum2, p2);
-                            w[i] = pack_bf16x2(f32x2_lo(p2), f32x2_hi(p2));
+                            for (int i = 2; i < 16; i += 2)
+                                mx[c] = max3_nan(mx[c], __uint_as_float(y[i - 1]), __uint_as_float(y[i]));
                         }
-                        tmem_st_x16(t_s + 16 * c, w);
+                        float top = max3_nan(max3_nan(mx[0], mx[1], __uint_as_float(x[0][15])),
+                                             max3_nan(mx[2], mx[3], __uint_as_float(x[0][31])),
+                                             max3_nan(__uint_as_float(x[1][15]), __uint_as_float(x[1][31]), kNegInf)) *
+                                    a.scale_log2;
+                        if (!(top < __int_as_float(0x7f800000))) top = __int_as_float(0x7fc00000);   // an infinite score: NaN
+                        if (!begun) {
+                            m = top;
+                            begun = true;
+                        } else {
+                            // the running max moves only when a half tile exceeds it by more than 2^32
+                            const bool up = live && !(top <= m + kAttnLazy);
+                            if (__any_sync(0xFFFFFFFFu, up)) {
+                                const float alpha = up ? attn_exp2(m - top) : 1.f;
+                                if (up) m = top;
+                                l *= alpha;
+                                // the product before this one has landed in O
+                                if (half == 0)
+                                    cta_wait(&bar[kTbSFull + 2 * wg + 1], done & 1, s_abort);
+                                else
+                                    cta_wait(&bar[kTbPvA + wg], done & 1, s_abort);
+                                __syncwarp();
+                                tc_fence_after_sync();
+#pragma unroll 1
+                                for (int c = 0; c < 8; ++c) {
+                                    uint32_t o[16];
+                                    tmem_ld_x16(t_o + wg * 128 + 16 * c, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                    tmem_st_x16(t_o + wg * 128 + 16 * c, o);
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                        const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2), m2 = f32x2(-m, -m);
+                        uint64_t sum2 = 0ull;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t y =
+                                    fma_f32x2(f32x2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, m2);
+                                const uint64_t p2 = i % kTaPolyEvery == kTaPolyEvery - 1
+                                                        ? exp2_poly_f32x2(y)
+                                                        : f32x2(attn_exp2(f32x2_lo(y)), attn_exp2(f32x2_hi(y)));
+                                sum2 = add_f32x2(sum2, p2);
+                                w[i] = pack_bf16x2(f32x2_lo(p2), f32x2_hi(p2));
+                            }
+                            tmem_st_x16(t_x + 16 * c, w);
+                        }
+                        l += f32x2_lo(sum2) + f32x2_hi(sum2);
+                        tmem_st_wait();
                     }
-                    l += f32x2_lo(sum2) + f32x2_hi(sum2);
-                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[kTbPFull + 2 * wg + half]);
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar[kTbPFull + wg]);
-                    if (k == 0 && wg == 0 && sq.count() >= kTaStagger) mbar_arrive(&bar[kTbStagger]);
-                }
-                ++done;
             }
             segs[0] += sq.count_of(0) > 0;
             segs[1] += sq.count_of(1) > 0;
