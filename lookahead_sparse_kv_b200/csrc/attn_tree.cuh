@@ -19,8 +19,11 @@
 // Two softmax warpgroups keep the tensor core and the exponentials busy at
 // once: step s of a segment belongs to warpgroup s & 1.  Its 128 tokens go in two
 // halves: while the second half's weights are made, the first half's product and
-// S of the first half of step s + 2 run (whole steps left each warpgroup waiting
-// for its own two MMAs, 3,650 cycles a KV tile of two row tiles).  With two row tiles (an item's
+// S of the first half of step s + 2 run.  (S of 64 tokens takes 51 cycles an MMA
+// where 128 take 67, as the query rows are read from shared memory twice as
+// often; but whole steps left each warpgroup waiting for its own two MMAs, and the
+// 16 x 64-node case at 104 us instead of 87.  Handing the exponentials from one
+// warpgroup to the other by turns changed nothing.)  With two row tiles (an item's
 // 256 rows) steps 2i and 2i + 1 are the two row tiles on KV tile i, so a KV tile
 // is read once for both; with one row tile (128 rows or fewer) they are KV tiles
 // 2i and 2i + 1, each warpgroup with its own O, joined at the end.
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int bar_full = is_k ? kTbKFull : kTbVFull, bar_empty = is_k ? kTbKEmpty : kTbVEmpty;
             prefetch_tensormap(tm);
             prefetch_tensormap(tt);
-            const uint64_t pol = a.pairs > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+            const uint64_t pol = l2_policy_evict_first();
             int pos = 0;
             int last[2] = {-1, -1};
             for (int p = 0;; ++p) {
