@@ -56,9 +56,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (StepSync, append_kv, block_overlap, build_summaries, decode_layer_step, evict_slots, make_dims,
+from . import (Layer, StepSync, append_kv, block_overlap, build_summaries, decode_layer_step, evict_slots, make_dims,
                make_layer, plan_fetch, plan_fetch_at, prefetch, score_select_plan, score_select_rows, sparse_attn,
                step_advance, workspace_bytes)
+from .tree import commit_path, qk_norm_rope, tree_attn, tree_layout, tree_workspace_bytes, verify_tree
 
 HEAD_DIM, BLOCK_TOKENS = 128, 16
 
@@ -324,3 +325,78 @@ class DecodePipeline:
             return
         for L in self.layers:
             self.main.wait_event(L.fetch_done)
+
+
+class TreeDecoder:
+    """Speculative steps with a draft tree over a DecodePipeline's layers.
+
+    A step, all on the pipeline's main stream (the model's own work between the calls runs there too):
+
+        begin(parent, n_nodes)              visibility words and positions, once
+        out = layer(i, qkv)                 per layer: norms and rotation of the projection rows, attention of the
+                                            nodes over the resident blocks and the tree, then the scores, top-K and
+                                            plan of the layer's next working set from the nodes' queries, and its
+                                            gather on the copy stream (OasisKV Figure 8)
+        next_token = verify(probs, ...)     which nodes stand, and the token after them
+        commit()                            their keys and values into every layer's host KV, summaries and pool
+
+    n_tree >= d.n_queries; the selection takes the first n_queries nodes (node 0 counts as the verification row).
+    Rows of padding nodes take part in it, so they should hold copies of a real row.  As with appended tokens, a
+    block that a commit opens is attended once a later plan has made it resident.
+    """
+
+    def __init__(self, pipe: DecodePipeline, n_tree: int, inv_freq: torch.Tensor, eps: float = 1e-6, wq=None, wk=None):
+        d, L = pipe.d, len(pipe.layers)
+        assert n_tree >= d.n_queries and pipe.exact is None and pipe.step_dev is None
+        self.pipe, self.T, self.inv_freq, self.eps = pipe, n_tree, inv_freq, eps
+        self.wq, self.wk = wq or [None] * L, wk or [None] * L
+        dev = inv_freq.device
+        B, Hq, Hkv = d.batch, d.n_q_heads, d.n_kv_heads
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.q = torch.empty((B, n_tree, Hq, HEAD_DIM), **bf)
+        self.k_tree, self.v_tree = (torch.empty((L, B, Hkv, n_tree, HEAD_DIM), **bf) for _ in range(2))
+        self.out = torch.empty((B, n_tree, Hq, HEAD_DIM), **bf)
+        self.lse = torch.empty((B, n_tree, Hq), dtype=torch.float32, device=dev)
+        self.mask = torch.zeros((B, n_tree), dtype=torch.int64, device=dev)
+        self.pos, self.path = torch.zeros((B, n_tree), **i32), torch.full((B, n_tree), -1, **i32)
+        self.n_accept, self.next_token = torch.zeros(B, **i32), torch.full((B,), -1, **i32)
+        self.ws = torch.empty(tree_workspace_bytes(d, n_tree), dtype=torch.uint8, device=dev)
+        self.table = (Layer * L)(*(pipe._native_layer(i, x) for i, x in enumerate(pipe.layers)))
+        self.step = 0
+
+    def begin(self, parent, n_nodes=None):
+        p = self.pipe
+        self.parent, self.n_nodes = parent, n_nodes
+        self.step += 1
+        tree_layout(p.d, self.T, parent, n_nodes, p.ctx_len, self.mask, self.pos, stream=p.main)
+
+    def layer(self, i, qkv) -> torch.Tensor:
+        """Layer i over its projection rows [B, T, >= (Hq + 2 Hkv) * 128]; returns out, valid until the next layer."""
+        p = self.pipe
+        d, L = p.d, p.layers[i]
+        qk_norm_rope(d, self.T, qkv, self.wq[i], self.wk[i], self.eps, self.inv_freq, self.pos, self.q, self.k_tree[i],
+                     self.v_tree[i], stream=p.main)
+        p.main.wait_event(L.fetch_done)                # the working set that the last step planned
+        tree_attn(d, self.T, self.q, L.pool, L.slot_table, p.ctx_len, self.k_tree[i], self.v_tree[i], self.mask, p.scale,
+                  self.out, self.lse, self.ws, stream=p.main)
+        rows = self.q
+        if self.T > d.n_queries:
+            with torch.cuda.stream(p.main):
+                rows = self.q[:, :d.n_queries].contiguous()
+        p._select_plan_fetch(i, L, rows, self.step, p.ctx_len)
+        return self.out
+
+    def verify(self, probs, tokens, u_accept, u_sample, draft_probs=None) -> torch.Tensor:
+        verify_tree(self.pipe.d, self.T, probs, draft_probs, tokens, self.parent, self.n_nodes, u_accept, u_sample, self.path,
+                    self.n_accept, self.next_token, stream=self.pipe.main)
+        return self.next_token
+
+    def commit(self):
+        """After every layer's gather, which reads the host blocks and writes the slots that this call extends."""
+        p = self.pipe
+        for L in p.layers:
+            p.main.wait_event(L.fetch_done)
+        commit_path(p.d, self.T, self.table, self.k_tree, self.v_tree, self.path, self.n_accept, p.ctx_len, p.ctx[1 - p.cur],
+                    stream=p.main)
+        p.cur = 1 - p.cur
