@@ -299,8 +299,9 @@ int oasis_commit_path(const oasis_dims* dp, int32_t n_tree, const oasis_layer* l
     if (int rc = check_ptr(ctx_len_out, "ctx_len_out", true)) return rc;
     if (ctx_len_out != nullptr && ctx_len_out == ctx_len)
         return fail(OASIS_EINVAL, "ctx_len_out must not alias ctx_len");
-    // every layer is checked before the first launch
-    for (int i = 0; i < n_layers; ++i) {
+    // Every layer is checked before the first launch; the addresses of up to 64 are kept from that.
+    oasis::CommitLayers c = {};
+    auto take = [&](int i, int to) {
         const oasis_layer& L = layers[i];
         if (int rc = check_ptr(L.host_kv, "host_kv", true)) return rc;
         if (int rc = check_ptr(L.kmin, "kmin")) return rc;
@@ -313,24 +314,22 @@ int oasis_commit_path(const oasis_dims* dp, int32_t n_tree, const oasis_layer* l
         const void* hv = nullptr;
         if (L.host_kv != nullptr)
             if (int rc = device_view(L.host_kv, "host_kv", false, &hv)) return rc;
-    }
+        c.host[to] = static_cast<uint4*>(const_cast<void*>(hv));
+        c.pool[to] = static_cast<uint4*>(L.pool);
+        c.kmin[to] = static_cast<uint4*>(const_cast<void*>(L.kmin));
+        c.kmax[to] = static_cast<uint4*>(const_cast<void*>(L.kmax));
+        c.slot_table[to] = L.slot_table;
+        return static_cast<int>(OASIS_OK);
+    };
+    for (int i = 0; i < n_layers; ++i)
+        if (int rc = take(i, i % oasis::kCommitLayers)) return rc;
     static OncePerDevice once;
     if (int rc = once([] { return carveout(oasis::commit_path_kernel, "commit_path carve-out"); })) return rc;
     const size_t layer_rows = static_cast<size_t>(d.B) * d.Hkv * n_tree;
     for (int l0 = 0; l0 < n_layers; l0 += oasis::kCommitLayers) {
         const int nl = std::min(n_layers - l0, oasis::kCommitLayers);
-        oasis::CommitLayers c = {};
-        for (int i = 0; i < nl; ++i) {
-            const oasis_layer& L = layers[l0 + i];
-            const void* hv = nullptr;
-            if (L.host_kv != nullptr)
-                if (int rc = device_view(L.host_kv, "host_kv", false, &hv)) return rc;
-            c.host[i] = static_cast<uint4*>(const_cast<void*>(hv));
-            c.pool[i] = static_cast<uint4*>(L.pool);
-            c.kmin[i] = static_cast<uint4*>(const_cast<void*>(L.kmin));
-            c.kmax[i] = static_cast<uint4*>(const_cast<void*>(L.kmax));
-            c.slot_table[i] = L.slot_table;
-        }
+        for (int i = 0; i < nl && n_layers > oasis::kCommitLayers; ++i)
+            if (int rc = take(l0 + i, i)) return rc;
         const dim3 grid(static_cast<unsigned>(d.B * d.Hkv), static_cast<unsigned>(nl));
         oasis::commit_path_kernel<<<grid, oasis::kCommitThreads, 0, static_cast<cudaStream_t>(stream)>>>(
             c, d, n_tree, static_cast<const uint4*>(k_tree) + l0 * layer_rows * 16,
