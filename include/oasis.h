@@ -417,7 +417,7 @@ int oasis_tree_attn(const oasis_dims* d, int32_t n_tree, const void* q, const vo
  * [B] (how many: the root counts) and next_token int32 [B]; a sequence without
  * nodes gets 0 and -1.  A node whose token is outside [0, vocab) or whose
  * parent is outside [-1, j) never stands and sets OASIS_DEVERR_ID_RANGE.
- * 1 <= vocab <= 262144.  All device. */
+ * 1 <= vocab <= 2^30.  All device. */
 int oasis_verify_tree(const oasis_dims* d, int32_t n_tree, int32_t vocab, const float* probs, const float* draft_probs,
                       size_t row_stride, const int32_t* tokens, const int32_t* parent, const int32_t* n_nodes,
                       const float* u_accept, const float* u_sample, int32_t* path, int32_t* n_accept,

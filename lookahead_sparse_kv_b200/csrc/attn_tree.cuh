@@ -314,6 +314,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         __syncwarp();
         list_segment(0);
     }
+    if (warp == kTaLoader && lane == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_tk);
+        prefetch_tensormap(&tm_tv);
+    }
     if (warp == kTaMma) {
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
@@ -399,8 +406,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const CUtensorMap* tt = is_k ? &tm_tk : &tm_tv;
             uint8_t* ring = is_k ? sK : sV;
             const int bar_full = is_k ? kTbKFull : kTbVFull, bar_empty = is_k ? kTbKEmpty : kTbVEmpty;
-            prefetch_tensormap(tm);
-            prefetch_tensormap(tt);
             const uint64_t pol = l2_policy_evict_first();
             int pos = 0;
             int last[2] = {-1, -1};
@@ -431,7 +436,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             for (int st = 0; st < 2; ++st)
                 if (last[st] >= 0) mbar_wait(&bar[bar_full + st], static_cast<uint32_t>((last[st] >> 1) & 1));
         } else if (lane == 2) {
-            prefetch_tensormap(&tm_q);
             const uint64_t pol = l2_policy_evict_first();
             int nz = 0, loaded = -1;
             for (int p = 0;; ++p) {

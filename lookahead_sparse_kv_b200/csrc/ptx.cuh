@@ -107,6 +107,12 @@ __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gmem_src
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Waits until at most N of the thread's latest groups are still under way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Load with acquire semantics at GPU scope (pairs with a release by a
 // __threadfence() + atomic in another CTA).
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {

@@ -224,8 +224,7 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
                       int32_t* next_token, void* stream) {
     Dims d;
     if (int rc = check_tree(dp, n_tree, &d)) return rc;
-    if (vocab < 1 || vocab > oasis::kVerMaxVocab)
-        return fail(OASIS_EINVAL, "vocab must be in [1, %d] (got %d)", oasis::kVerMaxVocab, vocab);
+    if (vocab < 1 || vocab > (1 << 30)) return fail(OASIS_EINVAL, "vocab must be in [1, 2^30] (got %d)", vocab);
     if (row_stride < static_cast<size_t>(vocab) || row_stride > (size_t(1) << 40))
         return fail(OASIS_EINVAL, "row_stride must be >= vocab (got %zu)", row_stride);
     if (int rc = check_ptr(probs, "probs")) return rc;
@@ -240,8 +239,7 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
     if (int rc = check_ptr(next_token, "next_token")) return rc;
     static OncePerDevice once;
     if (int rc = once([] {
-            const int most = 2 * 16 * oasis::ver_cap(oasis::kVerMaxVocab, oasis::kVerMaxCluster);
-            if (int rc = set_smem(oasis::verify_tree_kernel, most, "verify_tree smem")) return rc;
+            if (int rc = set_smem(oasis::verify_tree_kernel, oasis::kVerSmem, "verify_tree smem")) return rc;
             const cudaError_t e =
                 cudaFuncSetAttribute(oasis::verify_tree_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             return e == cudaSuccess ? OASIS_OK : cuda_fail(e, "verify_tree cluster size");
@@ -262,13 +260,13 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
     a.B = d.B;
     a.T = n_tree;
     a.vocab = vocab;
-    // 16 CTAs a sequence where the rows are long: their shares of two rows then leave room for two CTAs an SM
-    const int cluster = vocab > 65536 ? 16 : 8;
-    const size_t smem = static_cast<size_t>(draft_probs != nullptr ? 2 : 1) * 16 * oasis::ver_cap(vocab, cluster);
+    // 16 CTAs a sequence where the rows are long and all sequences' CTAs find an SM of their own, else 8 (two CTAs
+    // fit an SM: 32 sequences' clusters of 8 run at once)
+    const int cluster = vocab > 65536 && 16ll * d.B <= sm_count() ? 16 : 8;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(d.B) * cluster);
     cfg.blockDim = dim3(oasis::kVerThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = oasis::kVerSmem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;

@@ -15,17 +15,22 @@
 // r_k is never stored.  Subtracting and cutting at 0 again and again is doing it
 // once with the sum, r_k = max(p - c_k d, 0), c_k = S_0 + .. + S_{k-1}, so a row is
 // always p, d and one number.  One cluster of 8 or 16 CTAs per sequence.  CTA 0
-// walks the tree on single entries gathered up front (all nodes' parents, tokens,
-// p and d at the token) and sends the others a command when a sum over the
-// vocabulary is needed: after a rejection with children left, and for the draw.
-// Each CTA keeps its share of the node's rows in shared memory, copied there with
-// all of its loads in flight at once, sums it, and pushes the sum to the peers;
-// further sums at the same node, and the draw, read no memory.  HBM bounds it at
-// many sequences (the rows p and d of the last node, once), latency at one: the
-// walk's gathers, a share of the row and three cluster barriers.
+// gathers single entries up front (all nodes' parents, tokens, p and d at the
+// token) and hands them to the others, so that every CTA walks the tree on the same
+// numbers (nothing else decides how often the cluster meets) and they agree when a
+// sum over the vocabulary is needed: after a rejection with children left, and for
+// the draw.
+// Each CTA sums its share of the row and pushes the sum to the peers.  Every lane
+// streams its entries through a ring of its own in shared memory (six stages of 32
+// bytes in flight, 96 KiB a CTA), so no load waits for another and no thread for
+// another's; rows are read again for each sum, from L2.  HBM bounds it at many
+// sequences (the rows p and d of the last node, once), latency at one: the walk's
+// gathers, a share of the row and two cluster barriers.
 #pragma once
 
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "common.cuh"
 #include "tree.cuh"
@@ -35,10 +40,8 @@ namespace oasis {
 constexpr int kVerMaxCluster = 16;
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kVerMaxVocab = 1 << 18;              // 16 CTAs hold two rows of as many in 131 KiB each
-
-// 16-byte groups of a row that a CTA holds at most (rows begin anywhere in a group).
-__host__ __device__ constexpr int ver_cap(int vocab, int cluster) { return ((vocab + 6) / 4 + cluster - 1) / cluster; }
+constexpr int kVerRing = 6;                        // stages of a lane's ring: 16 bytes of each row
+constexpr int kVerSmem = kVerThreads * kVerRing * 2 * 16;
 
 struct VerifyArgs {
     const float* probs;          // [B][T] rows of `vocab` floats, row_stride apart
@@ -57,7 +60,16 @@ struct VerifyArgs {
 
 struct VerifyCmd {
     double c;                                      // what of the draft's row is taken off
-    int cur, rounds, last;                         // node, rejections before this sum, whether the draw follows
+    int cur, rounds, last, count;                  // node, rejections before this sum, whether the draw follows, path so far
+};
+
+// What the walk looks at, the same in every CTA of a cluster.
+struct VerifyIn {
+    int token[kMaxTree];
+    float p[kMaxTree], d[kMaxTree], u[kMaxTree];   // the parent's rows at the token, and the node's number
+    unsigned int kids[kMaxTree][2];                // each node's children, a bit each
+    int n;
+    float u_sample;
 };
 
 // What is no positive finite number counts as 0.
@@ -76,29 +88,57 @@ __device__ __forceinline__ double ver_wide(float x) {
 }
 constexpr double kVerScale = 0x1p896;
 
-// A CTA's share of the row that is summed or drawn from, r after some
-// rejections at a node, in shared memory.  Rows are taken in 16-byte groups of 4
-// entries; a row begins anywhere (an odd vocabulary), so group g holds entries
-// 4g - off .. 4g - off + 3.
+// The row that is summed or drawn from, r after some rejections at a node.  It is
+// read in 16-byte groups of 4 entries; a row begins anywhere (an odd vocabulary),
+// so group g holds entries 4g - off .. 4g - off + 3.
 struct VerifyRow {
-    const float4 *p, *d;         // groups c_lo.. of the target's and the draft's row
-    double c;                    // r = max(p - c d, 0); 0: p
+    const float *p, *d;          // d: NULL without draft rows, or where none is needed
+    double c;                    // r = max(p - c d, 0)
     const int* gone;             // without draft rows: the tokens turned down
-    int n_gone, off, c_lo;
+    int n_gone, off, vocab;
 
-    // Copies groups [lo, hi) of a row to `to` (the calling warp's lanes; the ends entry by entry).
-    __device__ __forceinline__ void fetch(const float* r, int vocab, int lo, int hi, int lane, float4* to) const {
-        for (int g = lo + lane; g < hi; g += 32) {
-            const int i = 4 * g - off;
-            if (i >= 0 && i + 3 < vocab) {
-                cp_async_16(to + (g - c_lo), r + i);
-            } else {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = i + e >= 0 && i + e < vocab ? __ldg(r + i + e) : 0.f;
-                to[g - c_lo] = make_float4(v[0], v[1], v[2], v[3]);
-            }
+    // Starts copying this lane's group g of both rows to `to` (the ends of a row entry by entry).
+    __device__ __forceinline__ void fetch(int g, float4* to) const {
+        const int i = 4 * g - off;
+        if (i >= 0 && i + 3 < vocab) {
+            cp_async_16(to, p + i);
+            if (d != nullptr) cp_async_16(to + 32, d + i);
+            return;
         }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = i + e >= 0 && i + e < vocab;
+            v[e] = in ? __ldg(p + i + e) : 0.f;
+            v[4 + e] = in && d != nullptr ? __ldg(d + i + e) : 0.f;
+        }
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[32] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    // The warp's groups [lo, hi), 32 at a time in order, through this lane's ring: f(group, p, d) until it says stop.
+    // Without kClean they come as they are.
+    template <bool kClean, class F>
+    __device__ __forceinline__ void stream(int lo, int hi, int lane, float4* ring, F&& f) const {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kVerRing; ++s) {
+            const int g = lo + 32 * s + lane;
+            if (g < hi) fetch(g, ring + 64 * s);
+            cp_async_commit();
+        }
+        int at = 0;
+        for (int g0 = lo; g0 < hi; g0 += 32) {
+            cp_async_wait_group<kVerRing - 1>();
+            const int g = g0 + lane;
+            float4 pv = g < hi ? ring[64 * at] : zero;
+            float4 dv = g < hi && d != nullptr ? ring[64 * at + 32] : zero;
+            if (g + 32 * kVerRing < hi) fetch(g + 32 * kVerRing, ring + 64 * at);
+            cp_async_commit();
+            at = at + 1 == kVerRing ? 0 : at + 1;
+            if (kClean) settle(g0, lane, pv, dv);
+            if (f(g, pv, dv)) break;
+        }
+        cp_async_wait_all();
     }
     // r of an entry, times 2^-896, before it is cut at 0
     __device__ __forceinline__ double raw(float pv, float dv) const { return fma(-c, ver_wide(dv), ver_wide(pv)); }
@@ -106,18 +146,14 @@ struct VerifyRow {
         const double y = raw(pv, dv);
         return y > 0.0 ? y : 0.0;
     }
-    // Group g (zeros from hi on), 0 for what is no positive finite number and for tokens turned down; the warp's
-    // lanes hold consecutive groups.
-    __device__ __forceinline__ void get(int g, int hi, int lane, float4& pv, float4& dv) const {
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        pv = g < hi ? p[g - c_lo] : zero;
-        dv = c != 0.0 && g < hi ? d[g - c_lo] : zero;
+    // 0 for what is no positive finite number, and for tokens turned down
+    __device__ __forceinline__ void settle(int g0, int lane, float4& pv, float4& dv) const {
         if (__any_sync(0xFFFFFFFFu, max(top(pv), top(dv)) > 0x7F7FFFFFu)) {   // a sign, an infinity or NaN
             pv = sound(pv);
             dv = sound(dv);
         }
         for (int j = 0; j < n_gone; j += 32) {
-            const int e = j + lane < n_gone ? gone[j + lane] + off - 4 * (g - lane) : -1;
+            const int e = j + lane < n_gone ? gone[j + lane] + off - 4 * g0 : -1;
             unsigned hit = __ballot_sync(0xFFFFFFFFu, e >= 0 && e < 128);
             for (; hit != 0; hit &= hit - 1) {
                 const int at = __shfl_sync(0xFFFFFFFFu, e, __ffs(hit) - 1);
@@ -155,13 +191,12 @@ __device__ __forceinline__ double warp_sum(double v) {
 __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const VerifyArgs a) {
     namespace cg = cooperative_groups;
     cg::cluster_group cl = cg::this_cluster();
-    __shared__ int s_token[kMaxTree], s_path[kMaxTree];
-    __shared__ float s_u[kMaxTree], s_p[kMaxTree], s_d[kMaxTree];
-    __shared__ unsigned int s_kids[kMaxTree][2];   // each node's children, a bit each
+    __shared__ VerifyIn s_in;
+    __shared__ int s_path[kMaxTree];
     __shared__ int s_gone[kMaxTree];               // without draft rows: tokens turned down at this node
     __shared__ VerifyCmd s_cmd;
     __shared__ double s_part[2][kVerMaxCluster];   // the CTAs' sums of a pass, two passes deep
-    extern __shared__ float4 s_rows[];             // the shares of p and d
+    extern __shared__ float4 s_rings[];
     __shared__ double s_warp[kVerWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(cl.block_rank());
@@ -170,18 +205,21 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
     const int T = a.T;
     const bool has_draft = a.draft != nullptr;
     const long long row0 = static_cast<long long>(b) * T;
-    int par = -1, x = -1;
-    if (rank == 0 && tid < T) {                    // (in flight together with the count)
-        par = a.parent[row0 + tid];
-        x = a.tokens[row0 + tid];
-        s_kids[tid][0] = s_kids[tid][1] = 0u;
-    }
-    int n = a.n_nodes != nullptr ? a.n_nodes[b] : T;
-    if (n < 0 || n > T) {
-        if (rank == 0 && tid == 0) raise_dev_error(OASIS_DEVERR_ID_RANGE);
-        n = n < 0 ? 0 : T;
-    }
+    // (a peer's shared memory may be written once that peer runs: its arrival here says so)
+    auto started = cl.barrier_arrive();
+    int n = 0;
     if (rank == 0) {
+        int par = -1, x = -1;
+        if (tid < T) {                             // (in flight together with the count)
+            par = a.parent[row0 + tid];
+            x = a.tokens[row0 + tid];
+            s_in.kids[tid][0] = s_in.kids[tid][1] = 0u;
+        }
+        n = a.n_nodes != nullptr ? a.n_nodes[b] : T;
+        if (n < 0 || n > T) {
+            if (tid == 0) raise_dev_error(OASIS_DEVERR_ID_RANGE);
+            n = n < 0 ? 0 : T;
+        }
         __syncthreads();
         if (tid < T) {
             const int j = tid;
@@ -193,110 +231,118 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
                 const long long at = (row0 + par) * a.row_stride + x;
                 pj = a.probs[at];
                 if (has_draft) dj = a.draft[at];
-                atomicOr(&s_kids[par][j >> 5], 1u << (j & 31));
+                atomicOr(&s_in.kids[par][j >> 5], 1u << (j & 31));
             }
-            s_token[j] = x;
-            s_p[j] = pj;
-            s_d[j] = dj;
-            s_u[j] = a.u_accept[row0 + j];
-            s_path[j] = j == 0 && n > 0 ? 0 : -1;
+            s_in.token[j] = x;
+            s_in.p[j] = pj;
+            s_in.d[j] = dj;
+            s_in.u[j] = a.u_accept[row0 + j];
+        }
+        if (tid == 0) {
+            s_in.n = n;
+            s_in.u_sample = a.u_sample[b];
         }
         __syncthreads();
     }
-    // the walk (CTA 0's thread 0): current node, its children not tested yet, S and the sum of the S before
+    cl.barrier_wait(std::move(started));
+    if (rank == 0) {
+        constexpr int kWords = sizeof(VerifyIn) / 4;
+        for (int i = tid; i < kWords * (cta - 1); i += kVerThreads) {
+            const int w = i % kWords;
+            reinterpret_cast<uint32_t*>(cl.map_shared_rank(&s_in, 1 + i / kWords))[w] = reinterpret_cast<const uint32_t*>(&s_in)[w];
+        }
+    }
+    cl.sync();
+    n = s_in.n;
+
+    // the walk (thread 0): current node, its children not tested yet, S and the sum of the S before
     int cur = 0, count = 1, rounds = 0;
     uint64_t kids = 0;
     double S = 1.0, c_off = 0.0;
-    if (rank == 0) kids = s_kids[0][0] | (static_cast<uint64_t>(s_kids[0][1]) << 32);
+    if (tid == 0) {
+        kids = s_in.kids[0][0] | (static_cast<uint64_t>(s_in.kids[0][1]) << 32);
+        s_path[0] = 0;
+    }
     double total = 0.0, before = 0.0;              // (times 2^-896)
     int slot = 0;
     VerifyRow row;
     row.gone = s_gone;
-    row.p = s_rows;
-    row.d = s_rows + ver_cap(a.vocab, cta);
+    row.vocab = a.vocab;
+    float4* const ring = s_rings + warp * 64 * kVerRing + lane;   // [stage][row][lane]
     int w_lo = 0, w_hi = 0;                        // the groups that this warp sums
-    int have = -1;                                 // node whose rows are here
     while (true) {
-        if (rank == 0) {
-            if (tid == 0) {
-                VerifyCmd c;
-                c.last = 1;
-                while (kids != 0) {
-                    const int j = __ffsll(static_cast<long long>(kids)) - 1;
-                    kids &= kids - 1;
-                    double p = ver_clean(s_p[j]), dq = 1.0;
-                    if (has_draft) {
-                        dq = ver_clean(s_d[j]);
-                        p = fma(-c_off, dq, p);
-                    } else {
-                        for (int i = 0; i < rounds; ++i)
-                            if (s_gone[i] == s_token[j]) p = 0.0;
-                    }
-                    if (p > 0.0 && static_cast<double>(s_u[j]) * S * dq < p) {
-                        s_path[count++] = j;
-                        cur = j;
-                        kids = s_kids[j][0] | (static_cast<uint64_t>(s_kids[j][1]) << 32);
-                        rounds = 0;
-                        S = 1.0;
-                        c_off = 0.0;
-                        continue;
-                    }
-                    if (!has_draft) {
-                        s_gone[rounds++] = s_token[j];
-                        S -= p;
-                        continue;
-                    }
-                    // the sum after this rejection: for the next child, or for the draw
-                    ++rounds;
-                    c_off += S;
-                    c.last = kids == 0;
-                    break;
+        if (tid == 0) {
+            VerifyCmd c;
+            c.last = 1;
+            while (kids != 0) {
+                const int j = __ffsll(static_cast<long long>(kids)) - 1;
+                kids &= kids - 1;
+                double p = ver_clean(s_in.p[j]), dq = 1.0;
+                if (has_draft) {
+                    dq = ver_clean(s_in.d[j]);
+                    p = fma(-c_off, dq, p);
+                } else {
+                    for (int i = 0; i < rounds; ++i)
+                        if (s_gone[i] == s_in.token[j]) p = 0.0;
                 }
-                c.cur = cur;
-                c.rounds = rounds;
-                c.c = c_off;
-                s_cmd = c;
-            }
-            __syncthreads();
-            if (tid > 0 && tid < cta) {
-                *cl.map_shared_rank(&s_cmd, tid) = s_cmd;
+                if (p > 0.0 && static_cast<double>(s_in.u[j]) * S * dq < p) {
+                    s_path[count++] = j;
+                    cur = j;
+                    kids = s_in.kids[j][0] | (static_cast<uint64_t>(s_in.kids[j][1]) << 32);
+                    rounds = 0;
+                    S = 1.0;
+                    c_off = 0.0;
+                    continue;
+                }
                 if (!has_draft) {
-                    int* gone = cl.map_shared_rank(&s_gone[0], tid);
-                    for (int i = 0; i < s_cmd.rounds; ++i) gone[i] = s_gone[i];
+                    s_gone[rounds++] = s_in.token[j];
+                    S -= p;
+                    continue;
                 }
+                // the sum after this rejection: for the next child, or for the draw
+                ++rounds;
+                c_off += S;
+                c.last = kids == 0;
+                break;
             }
+            c.cur = cur;
+            c.rounds = rounds;
+            c.count = count;
+            c.c = c_off;
+            s_cmd = c;
         }
-        cl.sync();
+        __syncthreads();
         const VerifyCmd c = s_cmd;
         row.c = c.c;
         row.n_gone = has_draft ? 0 : c.rounds;
-        if (have != c.cur) {
-            // in order over CTAs and warps; a warp reads what it copied itself
-            const long long at = (row0 + c.cur) * a.row_stride;
-            row.off = static_cast<int>(at & 3);
-            const int groups = (a.vocab + row.off + 3) / 4;
-            const int per_cta = (groups + cta - 1) / cta;
-            const int c_hi = min(groups, (rank + 1) * per_cta);
-            row.c_lo = min(groups, rank * per_cta);
-            const int per_warp = (c_hi - row.c_lo + kVerWarps - 1) / kVerWarps;
-            w_lo = min(c_hi, row.c_lo + warp * per_warp);
-            w_hi = min(c_hi, w_lo + per_warp);
-            row.fetch(a.probs + at, a.vocab, w_lo, w_hi, lane, const_cast<float4*>(row.p));
-            if (c.c != 0.0) row.fetch(a.draft + at, a.vocab, w_lo, w_hi, lane, const_cast<float4*>(row.d));
-            have = c.cur;
-            cp_async_wait_all();
-            __syncwarp();
-        }
+        const long long at = (row0 + c.cur) * a.row_stride;
+        row.p = a.probs + at;
+        row.d = c.c != 0.0 ? a.draft + at : nullptr;
+        row.off = static_cast<int>(at & 3);
+        // in order over CTAs and warps
+        const int groups = (a.vocab + row.off + 3) / 4;
+        const int per_cta = (groups + cta - 1) / cta;
+        const int c_lo = min(groups, rank * per_cta), c_hi = min(groups, c_lo + per_cta);
+        const int per_warp = (c_hi - c_lo + kVerWarps - 1) / kVerWarps;
+        w_lo = min(c_hi, c_lo + warp * per_warp);
+        w_hi = min(c_hi, w_lo + per_warp);
         for (int again = 0;; ++again) {
-            double sum[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 2
-            for (int g0 = w_lo; g0 < w_hi; g0 += 32) {
-                float4 pv, dv;
-                row.get(g0 + lane, w_hi, lane, pv, dv);
+            double sum[4];
+            uint32_t most = 0;
+            auto add = [&](int, const float4& pv, const float4& dv) {
+                most = max(most, max(VerifyRow::top(pv), VerifyRow::top(dv)));
                 ver_add(sum[0], row.raw(pv.x, dv.x));
                 ver_add(sum[1], row.raw(pv.y, dv.y));
                 ver_add(sum[2], row.raw(pv.z, dv.z));
                 ver_add(sum[3], row.raw(pv.w, dv.w));
+                return false;
+            };
+            sum[0] = sum[1] = sum[2] = sum[3] = 0.0;
+            if (row.n_gone == 0) row.stream<false>(w_lo, w_hi, lane, ring, add);
+            // entries that are no positive finite numbers were taken for large ones: once more, looking at each
+            if (row.n_gone != 0 || __any_sync(0xFFFFFFFFu, most > 0x7F7FFFFFu)) {
+                sum[0] = sum[1] = sum[2] = sum[3] = 0.0;
+                row.stream<true>(w_lo, w_hi, lane, ring, add);
             }
             const double mine = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
             if (lane == 0) s_warp[warp] = mine;
@@ -315,6 +361,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
             }
             if (!c.last || total > 0.0 || c.rounds == 0 || again) break;
             row.c = 0.0;                           // nothing is left of the row: drawn from the row itself
+            row.d = nullptr;
             row.n_gone = 0;
             slot ^= 1;
         }
@@ -325,9 +372,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
     // No CTA touches another's shared memory from here on, so each may leave.
 
     if (rank == 0) {
-        if (tid < T) a.path[row0 + tid] = s_path[tid];
+        const int steps = n > 0 ? s_cmd.count : 0;
+        if (tid < T) a.path[row0 + tid] = tid < steps ? s_path[tid] : -1;
         if (tid == 0) {
-            a.n_accept[b] = n > 0 ? count : 0;
+            a.n_accept[b] = steps;
             if (n == 0 || !(total > 0.0)) a.next_token[b] = -1;
         }
     }
@@ -336,7 +384,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
     // that holds the crossing; sums are carried on in the same order level by
     // level, and a crossing that rounding hides from the last level is at the
     // last entry with mass.
-    const double t = fmax(static_cast<double>(a.u_sample[b]), 0.0) * total;
+    const double t = fmax(static_cast<double>(s_in.u_sample), 0.0) * total;
     int owner = -1;
     {
         double run = 0.0;
@@ -367,11 +415,9 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
     if (warp != wo) return;
     int found = -1, fallback = -1;
     double carry = base;
-    for (int g0 = w_lo; g0 < w_hi && found < 0; g0 += 32) {
-        float4 pv, dv;
-        row.get(g0 + lane, w_hi, lane, pv, dv);
+    row.stream<true>(w_lo, w_hi, lane, ring, [&](int g, const float4& pv, const float4& dv) {
         const double x[4] = {row.left(pv.x, dv.x), row.left(pv.y, dv.y), row.left(pv.z, dv.z), row.left(pv.w, dv.w)};
-        const int i = 4 * (g0 + lane) - row.off;
+        const int i = 4 * g - row.off;
         const double sum = (x[0] + x[1]) + (x[2] + x[3]);
         double inc = sum;
 #pragma unroll
@@ -395,7 +441,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_tree_kernel(const Verif
         if (has != 0) found = __shfl_sync(0xFFFFFFFFu, over, __ffs(has) - 1);
         if (some != 0) fallback = __shfl_sync(0xFFFFFFFFu, last, 31 - __clz(some));
         carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
-    }
+        return found >= 0;
+    });
     if (lane == 0) a.next_token[b] = found >= 0 ? found : fallback;
 }
 

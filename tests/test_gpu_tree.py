@@ -358,6 +358,23 @@ def test_verify_tree_same_token_twice_and_bad_tokens():
     assert lsk.read_device_error(clear=True) == lsk.DEVERR_ID_RANGE
 
 
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_tree_entries_that_are_no_probabilities(draft):
+    """Negative, infinite, NaN and subnormal entries in both rows, at nodes that reject, accept and draw: all but the subnormal ones
+    count as 0."""
+    B, T, V = 6, 9, 1201
+    g = torch.Generator().manual_seed(21)
+    p, q, tok, par, n, ua, us = verify_inputs(B, T, V, g, "tree", 0, noise=1.5, ragged=False)
+    for k, x in enumerate((float("inf"), float("-inf"), float("nan"), -0.25, -0.0, 1e-42)):
+        for t in (p, q):
+            at = torch.randint(0, V, (B, T, 5), generator=g)
+            t[..., :V].scatter_(2, at, x)
+    ref = TO.verify_tree(p.numpy(), q.numpy() if draft else None, tok.numpy(), par.numpy(), n.numpy(), ua.numpy(), us.numpy())
+    got = run_verify(p, q if draft else None, tok, par, n, ua, us, V)
+    for x, y in zip(got, ref):
+        assert np.array_equal(x, y), (x, y)
+
+
 def test_verify_tree_draws_with_the_targets_frequencies():
     """A chain of one draft over 4 tokens, 40,000 sequences: next tokens (the draft where it stands, else the draw) follow the
     target.  Counts are binomial: 5 standard deviations of 40,000 p (1 - p)."""

@@ -57,7 +57,7 @@ def call(L, name, d=None, **kw):
     ("tree_attn", "n_tree", -1, "n_tree"), ("tree_attn", "n_tree", 65, "n_tree"), ("tree_attn", "scale", 0.0, "scale"),
     ("tree_attn", "scale", float("inf"), "scale"), ("tree_attn", "scale", float("nan"), "scale"), ("tree_attn", "mask", None, "mask"),
     ("tree_attn", "v_tree", None, "v_tree"), ("tree_attn", "ws", None, "ws"), ("tree_attn", "ws_bytes", 100, "workspace"),
-    ("verify_tree", "vocab", 0, "vocab"), ("verify_tree", "vocab", 262145, "vocab"), ("verify_tree", "row_stride", 99, "row_stride"),
+    ("verify_tree", "vocab", 0, "vocab"), ("verify_tree", "vocab", (1 << 30) + 1, "vocab"), ("verify_tree", "row_stride", 99, "row_stride"),
     ("verify_tree", "probs", None, "probs"), ("verify_tree", "probs", 20, "probs is not"), ("verify_tree", "draft", 20, "draft_probs"),
     ("verify_tree", "u_sample", None, "u_sample"), ("verify_tree", "next_token", None, "next_token"), ("verify_tree", "n_tree", 0, "n_tree"),
     ("commit_path", "n_layers", 0, "n_layers"), ("commit_path", "layers", None, "layers"), ("commit_path", "path", None, "path"),
