@@ -295,6 +295,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         __syncwarp();
     };
 
+    // the joining kernel may take its place on the SMs; it waits there for this one's end
+    asm volatile("griddepcontrol.launch_dependents;");
+
     // ---------------------------------------------------------- set-up
     // (the first segment is listed meanwhile: its loads are the longest wait of the start)
     if (tid == 0) {
@@ -836,10 +839,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 // Joins the parts of the rows of split items: out = sum_k 2^(lse_k - M) o_k /
 // sum_k 2^(lse_k - M).  A warp a row, a part a lane for the weights, then a
-// float4 a lane for the channels.
+// float4 a lane for the channels.  Launched to start before the attention ends
+// (its CTAs fit beside one of the attention's), so its launch is not waited for.
 constexpr int kTjWarps = 4;
 __global__ void __launch_bounds__(32 * kTjWarps) tree_join_kernel(const Dims d, const TreeAttnArgs a) {
     const float kNegInf = -__int_as_float(0x7f800000);
+    asm volatile("griddepcontrol.wait;" ::: "memory");            // the attention has ended, its parts are written
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kTjWarps + (threadIdx.x >> 5);   // (b, node, head)
     if (row >= d.B * a.T * d.Hq) return;

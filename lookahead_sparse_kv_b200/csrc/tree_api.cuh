@@ -213,8 +213,20 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
     if (int rc = check_launch("tree_attn launch")) return rc;
     if (w.per % w.tpu == 0) return OASIS_OK;     // whole items
     const unsigned rows = static_cast<unsigned>(d.B) * n_tree * d.Hq;
-    oasis::tree_join_kernel<<<(rows + oasis::kTjWarps - 1) / oasis::kTjWarps, 32 * oasis::kTjWarps, 0,
-                              static_cast<cudaStream_t>(stream)>>>(d, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((rows + oasis::kTjWarps - 1) / oasis::kTjWarps);
+    cfg.blockDim = dim3(32 * oasis::kTjWarps);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, oasis::tree_join_kernel, d, a);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "tree_join launch");
+    }
     return check_launch("tree_join launch");
 }
 
