@@ -33,7 +33,8 @@
 // the sum of the weights is of the unrounded ones in fp32.  The output is
 // rounded to bf16 anyway, by as much again.
 //
-// Work split.  The KV tiles of all items stand in one row, and each CTA takes an
+// Work split.  The KV tiles of all items stand in one row (a unit's row tiles far
+// apart, so that they read its tiles at the same time and DRAM gives them once), and each CTA takes an
 // equal stretch of it (`per` tiles), so every SM has the same share whatever the
 // number of items.  An item that lies in one stretch is written directly; the
 // parts of others go to the workspace, normalised, with their log2-sum-exp, and
@@ -109,7 +110,7 @@ struct TreeAttnArgs {
     float scale_log2;
     int T;
     int nt;                      // nodes a row tile
-    int pairs;                   // items a unit
+    int units;                   // an item: one of a unit's pairs of row tiles, unit fastest
     int tpu;                     // KV tiles a unit, the tree's among them
     int per;                     // KV tiles a CTA
     int total;                   // KV tiles in all
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int lo = static_cast<int>(at) - item * a.tpu;
         const int hi = static_cast<int>(min(static_cast<long long>(a.tpu), lo + (end - at)));
         at += hi - lo;
-        const int u = item / a.pairs, pr = item - u * a.pairs;
+        const int pr = item / a.units, u = item - pr * a.units;
         const int b = u / d.Hkv;
         const int first = max(lo, 1) - 1, pool_hi = hi - 1;       // pool tiles: the unit's first tile is the tree's
         int blk[kAttnTileSlots];
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 const int* info = s_info + pb * kTaInfoInts;
                 const int n = info[kTiN];
                 if (n < 0) break;
-                const int u = info[kTiItem] / a.pairs;
+                const int u = info[kTiItem] % a.units;
                 for (int i = 0; i < n; ++i, ++pos) {
                     const int st = pos & 1;
                     const int first = info[16 + 4 * i];
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (n < 0) break;
                 if (n > 0) {
                     const int item = info[kTiItem];
-                    const int u = item / a.pairs, pr = item - u * a.pairs;
+                    const int pr = item / a.units, u = item - pr * a.units;
                     const int b = u / d.Hkv, h = u - b * d.Hkv;
                     const int tiles = (2 * pr + 1) * a.nt < a.T ? 2 : 1;
                     if (nz > 0) cta_wait(&bar[kTbQFree], (nz - 1) & 1, s_abort);
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int n = __shfl_sync(0xFFFFFFFFu, got ? info[kTiN] : -1, 0);
             if (n < 0) break;
             if (n > 0) {
-                const int pr = __shfl_sync(0xFFFFFFFFu, info[kTiItem], 0) % a.pairs;
+                const int pr = __shfl_sync(0xFFFFFFFFu, info[kTiItem], 0) / a.units;
                 const TaSteps sq{(2 * pr + 1) * a.nt < a.T ? 1 : 0, n};
                 const int mine = sq.count_of(wg);
                 const uint64_t q_desc =
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int n = got ? info[kTiN] : -1;
             if (named_bar_or(kTnVote, 256, n < 0 || *s_abort)) break;
             const int item = info[kTiItem];
-            const int u = item / a.pairs, pr = item - u * a.pairs;
+            const int pr = item / a.units, u = item - pr * a.units;
             const int b = u / d.Hkv, h = u - b * d.Hkv;
             const TaSteps sq{(2 * pr + 1) * a.nt < a.T ? 1 : 0, n};
             const int my_tile = 2 * pr + (sq.two ? wg : 0);
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(32 * kTjWarps) tree_join_kernel(const Dims d, 
     const int hq = row % d.Hq, bj = row / d.Hq;
     const int j = bj % a.T, b = bj / a.T;
     const int h = hq / G, tile = j / a.nt;
-    const int item = (b * d.Hkv + h) * a.pairs + (tile >> 1);
+    const int item = (tile >> 1) * a.units + b * d.Hkv + h;
     const int base = item * a.tpu;
     const int c0 = base / a.per, parts = (base + a.tpu - 1) / a.per - c0 + 1;
     if (parts == 1) return;                                       // written directly

@@ -204,7 +204,7 @@ int oasis_tree_attn(const oasis_dims* dp, int32_t n_tree, const void* q, const v
     a.scale_log2 = scale * 1.4426950408889634f;
     a.T = n_tree;
     a.nt = w.nt;
-    a.pairs = w.pairs;
+    a.units = d.B * d.Hkv;
     a.tpu = w.tpu;
     a.per = w.per;
     a.total = w.total;
