@@ -390,9 +390,10 @@ size_t oasis_tree_workspace_bytes(const oasis_dims* d, int32_t n_tree);
  * oasis_sparse_attn) and over the nodes of the tree itself: the row of node j
  * sees every valid token of every occupied slot and the nodes whose bits are
  * set in mask[b][j] (any words; bits at or above T are ignored).  A row whose
- * word is 0 sees nothing: out = 0, lse = -inf.  Infinities and NaN in nodes
- * that a row does not see do not reach it.  Softmax statistics and sums are
- * fp32; out is rounded once to bf16.  q, k_tree, v_tree, mask as above; out
+ * word is 0 sees nothing: out = 0, lse = -inf (as where every score is -inf).
+ * Infinities and NaN in nodes that a row does not see do not reach it.  Softmax statistics and sums are
+ * fp32; the weights are rounded to bf16 before they meet the values, and out once
+ * more.  q, k_tree, v_tree, mask as above; out
  * bf16 [B][T][Hq][D]; lse fp32 [B][T][Hq] (natural log).  Hq / Hkv <= 64.
  * All device; ws: oasis_tree_workspace_bytes(d, n_tree) bytes. */
 int oasis_tree_attn(const oasis_dims* d, int32_t n_tree, const void* q, const void* pool, const int32_t* slot_table,

