@@ -36,7 +36,9 @@ def _device():
     global _dev
     if _dev == -2:
         _dev = 0 if torch.cuda.is_available() else -1
-    return torch.cuda.current_device() if _dev == 0 else None
+        if _dev == 0:
+            torch.cuda.init()
+    return torch._C._cuda_getDevice() if _dev == 0 else None
 
 
 def _stream_of(stream, dev):
