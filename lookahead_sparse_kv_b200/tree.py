@@ -26,7 +26,6 @@ __all__ = ["tree_layout", "qk_norm_rope", "tree_workspace_bytes", "tree_attn", "
            "commit_path"]
 
 _BF16, _F32, _I32, _I64, _U64 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint64
-_WORDS = (_I64, _U64)                    # a visibility word's 64 bits, signed or not
 _byref = ctypes.byref
 _dev = -2                                # -2: not asked yet whether there is a device, -1: there is none
 
@@ -70,13 +69,12 @@ def _why(x, what, name, dtype, numel, dev):
 
 def _arg(x, what, name, dtype, numel, dev):
     """Address of a contiguous tensor of `numel` elements on the current device (raw addresses pass unchecked)."""
-    if x.__class__ is int:
-        return x
     try:
-        if x.dtype is dtype and x.is_contiguous() and x.numel() >= numel and x.get_device() == dev:
+        if x.dtype is dtype and x.get_device() == dev and x.is_contiguous() and x.numel() >= numel:
             return x.data_ptr()
     except AttributeError:
-        pass
+        if x.__class__ is int:
+            return x
     raise _why(x, what, name, dtype, numel, dev)
 
 
@@ -85,6 +83,10 @@ def _rows(x, what, name, dtype, rows, width, dev):
     if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.get_device() != dev:
         raise _why(x, what, name, dtype, 0, dev)
     shape, stride = x.shape, x.stride()
+    if len(shape) == 3:                          # the usual case: [B, T, W], or a slice of a wider one along W
+        b, t, n = shape
+        if t > 1 and n >= width and b * t == rows and stride[2] == 1 and stride[0] == t * stride[1]:
+            return x.data_ptr(), stride[1]
     if len(shape) < 2 or shape[-1] < width or x.numel() != rows * shape[-1]:
         raise _bad(what, f"{name} must be {rows} rows of at least {width} elements, got {tuple(shape)}")
     if shape[-1] > 1 and stride[-1] != 1:
@@ -101,31 +103,33 @@ def _rows(x, what, name, dtype, rows, width, dev):
     return x.data_ptr(), shape[-1] if step is None else step
 
 
-def _check(rc, what):
-    if rc != 0:
-        raise OasisError(rc, what, last_error())
+def _failed(rc, what):
+    return OasisError(rc, what, last_error())
 
 
-def _tree(d, n_tree, what):
+def _check_tree(n_tree, what):
     if not 1 <= n_tree <= 64:
         raise _bad(what, f"n_tree must be in [1, 64] (got {n_tree})")
-    return d.batch * n_tree
+
+
+def _word_type(mask):
+    """int64 words or uint64 ones (anything else is held against int64)."""
+    return _U64 if getattr(mask, "dtype", None) is _U64 else _I64
 
 
 def tree_layout(d: Dims, n_tree, parent, n_nodes, ctx_len, mask, pos, stream=None):
     """Visibility words (int64 or uint64 [B][T]) and positions (int32 [B][T]) from parents; n_nodes may be None."""
     w = "oasis_tree_layout"
     dev = _device()
-    n = _tree(d, n_tree, w)
+    _check_tree(n_tree, w)
     b = d.batch
-    _check(lib().oasis_tree_layout(
+    n = b * n_tree
+    rc = lib().oasis_tree_layout(
         _byref(d), n_tree, _arg(parent, w, "parent", _I32, n, dev),
         None if n_nodes is None else _arg(n_nodes, w, "n_nodes", _I32, b, dev), _arg(ctx_len, w, "ctx_len", _I32, b, dev),
-        _words(mask, w, n, dev), _arg(pos, w, "pos", _I32, n, dev), _stream_of(stream, dev)), w)
-
-
-def _words(mask, w, n, dev):
-    return _arg(mask, w, "mask", mask.dtype if getattr(mask, "dtype", None) in _WORDS else _I64, n, dev)
+        _arg(mask, w, "mask", _word_type(mask), n, dev), _arg(pos, w, "pos", _I32, n, dev), _stream_of(stream, dev))
+    if rc:
+        raise _failed(rc, w)
 
 
 def qk_norm_rope(d: Dims, n_tok, qkv, wq, wk, eps, inv_freq, pos, q, k, v, stream=None):
@@ -138,11 +142,13 @@ def qk_norm_rope(d: Dims, n_tok, qkv, wq, wk, eps, inv_freq, pos, q, k, v, strea
     n, hq, hkv = d.batch * n_tok, d.n_q_heads, d.n_kv_heads
     at, step = _rows(qkv, w, "qkv", _BF16, n, (hq + 2 * hkv) * 128, dev)
     kv = n * hkv * 128
-    _check(lib().oasis_qk_norm_rope(
+    rc = lib().oasis_qk_norm_rope(
         _byref(d), n_tok, at, step, None if wq is None else _arg(wq, w, "wq", _BF16, 128, dev),
         None if wk is None else _arg(wk, w, "wk", _BF16, 128, dev), eps, _arg(inv_freq, w, "inv_freq", _F32, 64, dev),
         _arg(pos, w, "pos", _I32, n, dev), _arg(q, w, "q", _BF16, n * hq * 128, dev), _arg(k, w, "k", _BF16, kv, dev),
-        _arg(v, w, "v", _BF16, kv, dev), _stream_of(stream, dev)), w)
+        _arg(v, w, "v", _BF16, kv, dev), _stream_of(stream, dev))
+    if rc:
+        raise _failed(rc, w)
 
 
 def tree_workspace_bytes(d: Dims, n_tree) -> int:
@@ -153,18 +159,21 @@ def tree_attn(d: Dims, n_tree, q, pool, slot_table, ctx_len, k_tree, v_tree, mas
     """out: bf16 [B, T, Hq, 128], lse: fp32 [B, T, Hq]; ws: any tensor of tree_workspace_bytes(d, n_tree) bytes."""
     w = "oasis_tree_attn"
     dev = _device()
-    n = _tree(d, n_tree, w)
+    _check_tree(n_tree, w)
     b, hq, hkv = d.batch, d.n_q_heads, d.n_kv_heads
+    n = b * n_tree
     slots = b * hkv * d.budget_blocks
     kv = n * hkv * 128
     if not isinstance(ws, torch.Tensor):
         raise _bad(w, "ws must be a tensor (its size is taken from it)")
-    _check(lib().oasis_tree_attn(
+    rc = lib().oasis_tree_attn(
         _byref(d), n_tree, _arg(q, w, "q", _BF16, n * hq * 128, dev), _arg(pool, w, "pool", _BF16, slots * 4096, dev),
         _arg(slot_table, w, "slot_table", _I32, slots, dev), _arg(ctx_len, w, "ctx_len", _I32, b, dev),
-        _arg(k_tree, w, "k_tree", _BF16, kv, dev), _arg(v_tree, w, "v_tree", _BF16, kv, dev), _words(mask, w, n, dev), scale,
+        _arg(k_tree, w, "k_tree", _BF16, kv, dev), _arg(v_tree, w, "v_tree", _BF16, kv, dev), _arg(mask, w, "mask", _word_type(mask), n, dev), scale,
         _arg(out, w, "out", _BF16, n * hq * 128, dev), _arg(lse, w, "lse", _F32, n * hq, dev),
-        _arg(ws, w, "ws", ws.dtype, 1, dev), ws.numel() * ws.element_size(), _stream_of(stream, dev)), w)
+        _arg(ws, w, "ws", ws.dtype, 1, dev), ws.numel() * ws.element_size(), _stream_of(stream, dev))
+    if rc:
+        raise _failed(rc, w)
 
 
 def verify_tree(d: Dims, n_tree, probs, draft_probs, tokens, parent, n_nodes, u_accept, u_sample, path, n_accept, next_token,
@@ -173,8 +182,9 @@ def verify_tree(d: Dims, n_tree, probs, draft_probs, tokens, parent, n_nodes, u_
     draft_probs None: the drafts were not drawn at random; n_nodes may be None."""
     w = "oasis_verify_tree"
     dev = _device()
-    n = _tree(d, n_tree, w)
+    _check_tree(n_tree, w)
     b = d.batch
+    n = b * n_tree
     at, step = _rows(probs, w, "probs", _F32, n, 1, dev)
     vocab = probs.shape[-1]
     draft = None
@@ -182,11 +192,13 @@ def verify_tree(d: Dims, n_tree, probs, draft_probs, tokens, parent, n_nodes, u_
         draft, dstep = _rows(draft_probs, w, "draft_probs", _F32, n, 1, dev)
         if draft_probs.shape[-1] != vocab or dstep != step:
             raise _bad(w, "draft_probs must have the vocabulary and the row stride of probs")
-    _check(lib().oasis_verify_tree(
+    rc = lib().oasis_verify_tree(
         _byref(d), n_tree, vocab, at, draft, step, _arg(tokens, w, "tokens", _I32, n, dev), _arg(parent, w, "parent", _I32, n, dev),
         None if n_nodes is None else _arg(n_nodes, w, "n_nodes", _I32, b, dev), _arg(u_accept, w, "u_accept", _F32, n, dev),
         _arg(u_sample, w, "u_sample", _F32, b, dev), _arg(path, w, "path", _I32, n, dev), _arg(n_accept, w, "n_accept", _I32, b, dev),
-        _arg(next_token, w, "next_token", _I32, b, dev), _stream_of(stream, dev)), w)
+        _arg(next_token, w, "next_token", _I32, b, dev), _stream_of(stream, dev))
+    if rc:
+        raise _failed(rc, w)
 
 
 def make_cache_layers(d: Dims, host_kv, kmin, kmax, slot_table, pool):
@@ -194,7 +206,9 @@ def make_cache_layers(d: Dims, host_kv, kmin, kmax, slot_table, pool):
     where no host copy is kept), kmin / kmax [L, B, Hkv, N, 128], slot_table [L, B, Hkv, K], pool [L, B, Hkv, K, 2, 16, 128]
     (slot_table and pool None: no pool).  The table keeps the tensors alive."""
     w = "make_cache_layers"
-    _check(lib().oasis_check_dims(_byref(d)), w)
+    rc = lib().oasis_check_dims(_byref(d))
+    if rc:
+        raise _failed(rc, w)
     dev = _device()
     if not isinstance(kmin, torch.Tensor) or kmin.dim() < 2:
         raise _bad(w, "kmin must be a tensor with a leading layer dim")
@@ -221,15 +235,18 @@ def commit_path(d: Dims, n_tree, layers, k_tree, v_tree, path, n_accept, ctx_len
     make_layer; k_tree, v_tree: bf16 [L, B, Hkv, T, 128]; ctx_len_out may be None."""
     w = "oasis_commit_path"
     dev = _device()
-    n = _tree(d, n_tree, w)
+    _check_tree(n_tree, w)
     b = d.batch
+    n = b * n_tree
     if not isinstance(layers, ctypes.Array):
         layers = (Layer * len(layers))(*layers)
     elif layers._type_ is not Layer:
         raise _bad(w, "layers must be a table of Layer")
     L = len(layers)
     kv = L * n * d.n_kv_heads * 128
-    _check(lib().oasis_commit_path(
+    rc = lib().oasis_commit_path(
         _byref(d), n_tree, layers, L, _arg(k_tree, w, "k_tree", _BF16, kv, dev), _arg(v_tree, w, "v_tree", _BF16, kv, dev),
         _arg(path, w, "path", _I32, n, dev), _arg(n_accept, w, "n_accept", _I32, b, dev), _arg(ctx_len, w, "ctx_len", _I32, b, dev),
-        None if ctx_len_out is None else _arg(ctx_len_out, w, "ctx_len_out", _I32, b, dev), _stream_of(stream, dev)), w)
+        None if ctx_len_out is None else _arg(ctx_len_out, w, "ctx_len_out", _I32, b, dev), _stream_of(stream, dev))
+    if rc:
+        raise _failed(rc, w)

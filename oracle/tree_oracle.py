@@ -62,7 +62,8 @@ def tree_attention(q, pool_k, pool_v, slot_table, ctx_len, k_tree, v_tree, mask,
                 kk, vv = np.concatenate([ck, k_tree[b, h, seen]]), np.concatenate([cv, v_tree[b, h, seen]])
                 x = kk @ q[b, j, h * G:(h + 1) * G].T * scale                     # [tokens, G]
                 m = x.max(0)
-                e = np.exp(x - m)
+                with np.errstate(invalid="ignore"):                               # (an infinite score: NaN)
+                    e = np.exp(x - m)
                 out[b, j, h * G:(h + 1) * G] = (e / e.sum(0)).T @ vv
                 lse[b, j, h * G:(h + 1) * G] = m + np.log(e.sum(0))
     return out, lse
