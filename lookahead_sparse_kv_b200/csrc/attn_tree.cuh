@@ -537,7 +537,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     __syncwarp();
                 }
                 if (mine < 2 && elect_one()) umma_commit(&bar[kTbQFree]);
-                if (nz > 0) ta_wait(&bar[kTbOFree], (nz - 1) & 1, s_abort);   // the last segment's O is read
+                // The last segment's O is read.  (Only where this issuer writes O: a segment of one tile and one row
+                // tile ends without the second issuer, which could then come here a whole phase late, and a parity
+                // that has come round again reads as not done.)
+                if (nz > 0 && mine > 0) ta_wait(&bar[kTbOFree], (nz - 1) & 1, s_abort);
                 uint32_t acc = 0u;                                // the first product overwrites O
                 for (int k = 0; k < mine; ++k, ++done) {
                     const int s = 2 * k + wg, i = sq.tile(s), vt = pos + i, st = vt & 1;

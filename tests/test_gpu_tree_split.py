@@ -1,0 +1,94 @@
+"""tree_attn's split of the work: CTAs that walk many segments (whole items, stretches cut after one tile, segments without a tile),
+row-tile pairs beside single row tiles, and items joined from many parts.  Every row is compared with fp64 on the device.
+
+Tolerance: a softmax weight is rounded to bf16, half a step 2^-8 of it, and the output once more: 2^-8 |o| + (2^-8 + 2^-16) A with A the
+weighted mean of |v|; lse: fp32 scores, a few 2^-24 sum |q_c k_c|, here below 1e-4."""
+
+import pytest
+import torch
+
+import lookahead_sparse_kv_b200 as lsk
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, I32 = torch.bfloat16, torch.int32
+SCALE = 128 ** -0.5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from lookahead_sparse_kv_b200 import build
+    build.build()
+    lsk.lib()
+    yield
+    assert lsk.read_device_error(clear=True) == 0
+
+
+class Call:
+    """One call's tensors.  kinds: per sequence "full" (random free slots), "free" (nothing resident) or "blind" (no row sees
+    anything), taken in turn."""
+
+    def __init__(self, B, T, hq, hkv, K, seed, kinds=("full",)):
+        g = torch.Generator(DEV).manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)  # noqa: E731
+        N = K + 3
+        self.T, self.d = T, lsk.make_dims(B, hq, hkv, N, K, 1, 0)
+        self.q, self.k, self.v = r(B, T, hq, 128), r(B, hkv, T, 128), r(B, hkv, T, 128)
+        self.pool = r(B, hkv, K, 2, 16, 128)
+        st = torch.rand(B, hkv, N, generator=g, device=DEV).argsort(-1)[..., :K]
+        st = torch.where(torch.rand(B, hkv, K, generator=g, device=DEV) < 0.15, -1, st).int()
+        self.ctx = (N * 16 - torch.randint(0, 40, (B,), generator=g, device=DEV)).int()
+        up = torch.full((B, T), -1, dtype=I32, device=DEV)
+        j = torch.arange(T, device=DEV)
+        up[:] = torch.where(j > 0, (torch.rand(B, T, generator=g, device=DEV) * j).floor().int(), -1)
+        self.mask, pos = torch.empty(B, T, dtype=torch.int64, device=DEV), torch.empty(B, T, dtype=I32, device=DEV)
+        lsk.tree_layout(self.d, T, up, None, self.ctx, self.mask, pos)
+        for b in range(B):
+            if kinds[b % len(kinds)] == "free":
+                st[b] = -1
+            if kinds[b % len(kinds)] == "blind":
+                self.mask[b] = 0
+        self.st = st
+        self.ws = torch.full((lsk.tree_workspace_bytes(self.d, T),), 255, dtype=torch.uint8, device=DEV)
+        self.out, self.lse = torch.full((B, T, hq, 128), 9.0, dtype=BF, device=DEV), torch.full((B, T, hq), 9.0, device=DEV)
+
+    def run(self, ws=None, stream=None):
+        lsk.tree_attn(self.d, self.T, self.q, self.pool, self.st, self.ctx, self.k, self.v, self.mask, SCALE, self.out, self.lse,
+                      self.ws if ws is None else ws, stream=stream)
+        return self.out, self.lse
+
+    def check(self):
+        self.run()
+        B, T, hq = self.lse.shape
+        hkv, K = self.st.shape[1:]
+        tok = torch.arange(16, device=DEV)
+        valid = ((self.st[..., None] >= 0) & (self.st[..., None] * 16 + tok < self.ctx.view(B, 1, 1, 1))).flatten(2)
+        sees = (self.mask[:, :, None] >> torch.arange(T, device=DEV) & 1).bool()
+        for b in range(B):                                       # a sequence at a time: a few MB of doubles
+            keys = torch.cat([self.pool[b, :, :, 0].flatten(1, 2), self.k[b]], 1).double()
+            vals = torch.cat([self.pool[b, :, :, 1].flatten(1, 2), self.v[b]], 1).double()
+            q = self.q[b].double().view(T, hkv, hq // hkv, 128).permute(1, 0, 2, 3)
+            x = torch.einsum("htgc,hsc->htgs", q, keys) * SCALE
+            on = torch.cat([valid[b, :, None].expand(-1, T, -1), sees[b].expand(hkv, -1, -1)], -1)
+            on = on & sees[b].any(-1)[None, :, None]             # a row whose word is 0 sees nothing at all
+            x = x.masked_fill(~on[:, :, None], float("-inf"))
+            lse = torch.logsumexp(x, -1)
+            w = torch.exp(x - torch.where(lse.isinf(), 0.0, lse)[..., None])
+            o, size = (torch.einsum("htgs,hsc->htgc", w, y) for y in (vals, vals.abs()))
+            o, size = (y.permute(1, 0, 2, 3).reshape(T, hq, 128) for y in (o, size))
+            lse = lse.permute(1, 0, 2).reshape(T, hq)
+            over = (self.out[b].double() - o).abs() - (2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -16) * size + 1e-30)
+            assert not bool((over > 0).any()), (b, over.max())
+            fin = lse.isfinite()
+            assert torch.equal(self.lse[b].isfinite(), fin) and bool((self.lse[b][~fin] == float("-inf")).all())
+            assert float((self.lse[b].double() - lse)[fin].abs().max() if fin.any() else 0.0) <= 1e-4, b
+
+
+@pytest.mark.parametrize("B,T,hq,hkv,K,kinds", [
+    (200, 8, 8, 8, 8, ("free", "full", "blind", "free")),        # one tile, two or none, 13 items a CTA
+    (64, 8, 8, 8, 5, ("full",)), (90, 3, 16, 8, 1, ("free", "free", "full")),
+    (1, 7, 32, 8, 128, ("full",)),                               # stretches of two tiles over 17: cut after one
+    (5, 8, 8, 8, 128, ("full", "free", "full", "blind", "full"))])
+def test_segments_of_one_tile(B, T, hq, hkv, K, kinds):
+    """One row tile and one KV tile: the second issuer has nothing to do in such a segment and may be any time late in it."""
+    Call(B, T, hq, hkv, K, seed=B + K, kinds=kinds).check()
