@@ -126,6 +126,9 @@ class DecodePipeline:
         self.step_dev = torch.zeros(4, dtype=torch.int32, device=device) if device_step else None
         self.graph = None
         self._step_host = 0
+        # LRU stamps of a pipeline that draft-tree steps share: the last plain step, the newest stamp, and how far stamps
+        # run ahead of plain step numbers
+        self._plain, self._newest, self._ahead = 0, 0, 0
         self.exact = exact
         self.victims = victims
         if victims == "score":
@@ -236,8 +239,17 @@ class DecodePipeline:
 
     def prime(self, q_per_layer):
         """Step 0: select, plan and fetch from the drafts before decoding starts."""
+        self._plain = 0
+        stamp = self.next_stamp() if self._ahead else 0
         for i, (L, q) in enumerate(zip(self.layers, q_per_layer)):
-            self._select_plan_fetch(i, L, q, None if self.step_dev is not None else 0, self.ctx_len)
+            self._select_plan_fetch(i, L, q, None if self.step_dev is not None else stamp, self.ctx_len)
+
+    def next_stamp(self) -> int:
+        """LRU stamp of a step that has no number of its own (a draft-tree step): newer than every one given so far;
+        the plain steps that follow are stamped newer still."""
+        self._newest += 1
+        self._ahead = self._newest - self._plain
+        return self._newest
 
     def step(self, t, q_per_layer, appended=None, evict=None, inputs_ready=None, layer_done=None):
         """Decode step t >= 1: per layer [append] -> attention -> [loss] -> select/plan/fetch.
@@ -268,6 +280,10 @@ class DecodePipeline:
                 assert t == self._step_host + 1, "device-step pipelines take consecutive steps"
                 self._step_host = t
             step_advance(self.step_dev, stream=main)
+        elif t is not None:
+            self._plain = t
+            t += self._ahead
+            self._newest = max(self._newest, t)
         if appended is None:
             ctx_in = ctx = self.ctx_len
         else:
@@ -342,7 +358,9 @@ class TreeDecoder:
 
     n_tree >= d.n_queries; the selection takes the first n_queries nodes (node 0 counts as the verification row).
     Rows of padding nodes take part in it, so they should hold copies of a real row.  As with appended tokens, a
-    block that a commit opens is attended once a later plan has made it resident.
+    block that a commit opens is attended once a later plan has made it resident.  Several decoders (of other widths) and
+    the pipeline's own step() may take turns: the pipeline numbers all their steps in one order, which the LRU victim
+    order follows.
     """
 
     def __init__(self, pipe: DecodePipeline, n_tree: int, inv_freq: torch.Tensor, eps: float = 1e-6, wq=None, wk=None):
@@ -368,7 +386,7 @@ class TreeDecoder:
     def begin(self, parent, n_nodes=None):
         p = self.pipe
         self.parent, self.n_nodes = parent, n_nodes
-        self.step += 1
+        self.step = p.next_stamp()
         tree_layout(p.d, self.T, parent, n_nodes, p.ctx_len, self.mask, self.pos, stream=p.main)
 
     def layer(self, i, qkv) -> torch.Tensor:
