@@ -304,9 +304,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         __syncwarp();
     };
 
-    // the joining kernel may take its place on the SMs; it waits there for this one's end
-    asm volatile("griddepcontrol.launch_dependents;");
-
     // ---------------------------------------------------------- set-up
     // (the first segment is listed meanwhile: its loads are the longest wait of the start)
     if (tid == 0) {
@@ -410,6 +407,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (s_info[(pb ^ 1) * kTaInfoInts + kTiN] < 0) break;
             __syncwarp();
         }
+        // The last tile is under way: the joining kernel may take its place on the SMs and wait there for this one's
+        // end.  (Not earlier: its CTAs would fill the SMs left to a gather, which then ran behind the attention.)
+        asm volatile("griddepcontrol.launch_dependents;");
     } else if (warp == kTaLoader) {
         // ======================================================= loader
         if (lane < 2) {
@@ -853,8 +853,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 // Joins the parts of the rows of split items: out = sum_k 2^(lse_k - M) o_k /
 // sum_k 2^(lse_k - M).  A warp a row, a part a lane for the weights, then a
-// float4 a lane for the channels.  Launched to start before the attention ends
-// (its CTAs fit beside one of the attention's), so its launch is not waited for.
+// float4 a lane for the channels.  Launched once every CTA of the attention is at
+// its last tile (its CTAs fit beside one of the attention's), so its launch is not
+// waited for.
 constexpr int kTjWarps = 4;
 __global__ void __launch_bounds__(32 * kTjWarps) tree_join_kernel(const Dims d, const TreeAttnArgs a) {
     const float kNegInf = -__int_as_float(0x7f800000);

@@ -92,3 +92,32 @@ class Call:
 def test_segments_of_one_tile(B, T, hq, hkv, K, kinds):
     """One row tile and one KV tile: the second issuer has nothing to do in such a segment and may be any time late in it."""
     Call(B, T, hq, hkv, K, seed=B + K, kinds=kinds).check()
+
+
+def test_a_gather_runs_beside_a_split_call():
+    """The attention leaves SMs to a gather on another stream, and the kernel that joins the parts does not take them while it waits:
+    a gather that gets ready early in the call ends well before it (1 MB against 0.8 GB; the median of nine)."""
+    c = Call(12, 8, 64, 8, 1024, seed=2)
+    g = torch.Generator().manual_seed(3)
+    d = lsk.make_dims(1, 8, 8, 64, 64, 1, 16)
+    host = torch.randn(1, 8, 64, 2, 16, 128, generator=g).to(BF).pin_memory()
+    slot = torch.arange(16, dtype=I32, device=DEV).expand(1, 8, 16).contiguous()
+    n, pool = torch.full((1, 8), 16, dtype=I32, device=DEV), torch.empty(1, 8, 64, 2, 16, 128, dtype=BF, device=DEV)
+    copy = torch.cuda.Stream(priority=torch.cuda.Stream.priority_range()[1])
+    share = []
+    for i in range(12):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200000)                                # both streams are filled before either starts
+        ev[0].record()
+        copy.wait_event(ev[0])
+        with torch.cuda.stream(copy):
+            torch.cuda._sleep(40000)                             # the call is under way
+            lsk.prefetch(d, host, slot, slot, n, pool, stream=copy)
+            ev[1].record(copy)
+        c.run()
+        ev[2].record()
+        torch.cuda.synchronize()
+        share.append(ev[0].elapsed_time(ev[1]) / ev[0].elapsed_time(ev[2]))
+    assert torch.equal(pool[:, :, :16].cpu(), host[:, :, :16])
+    assert sorted(share[3:])[4] < 0.9, share
