@@ -249,14 +249,39 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
     if (int rc = check_ptr(path, "path")) return rc;
     if (int rc = check_ptr(n_accept, "n_accept")) return rc;
     if (int rc = check_ptr(next_token, "next_token")) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(oasis::kVerThreads);
+    cfg.dynamicSmemBytes = oasis::kVerSmem;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = oasis::kVerMaxCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    // How many clusters of 16 the device holds at once: more than 8 CTAs are not promised (0 where a partition's SMs are
+    // too few), and those that do not fit would run one after another.
     static OncePerDevice once;
-    if (int rc = once([] {
+    static int wide_on[64];
+    int wide = 0;
+    if (int rc = once([&] {
             if (int rc = set_smem(oasis::verify_tree_kernel, oasis::kVerSmem, "verify_tree smem")) return rc;
             const cudaError_t e =
                 cudaFuncSetAttribute(oasis::verify_tree_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            return e == cudaSuccess ? OASIS_OK : cuda_fail(e, "verify_tree cluster size");
+            if (e != cudaSuccess) return cuda_fail(e, "verify_tree cluster size");
+            cfg.gridDim = dim3(oasis::kVerMaxCluster);
+            if (cudaOccupancyMaxActiveClusters(&wide, oasis::verify_tree_kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                wide = 0;
+            }
+            int dev = 0;
+            if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) wide_on[dev] = wide;
+            return static_cast<int>(OASIS_OK);
         }))
         return rc;
+    if (wide == 0) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) wide = wide_on[dev];
+    }
     oasis::VerifyArgs a;
     a.probs = probs;
     a.draft = draft_probs;
@@ -273,19 +298,13 @@ int oasis_verify_tree(const oasis_dims* dp, int32_t n_tree, int32_t vocab, const
     a.T = n_tree;
     a.vocab = vocab;
     // 16 CTAs a sequence where the rows are long and all sequences' CTAs find an SM of their own, else 8 (two CTAs
-    // fit an SM: 32 sequences' clusters of 8 run at once)
-    const int cluster = vocab > 65536 && 16ll * d.B <= sm_count() ? 16 : 8;
-    cudaLaunchConfig_t cfg = {};
+    // fit an SM: 32 sequences' clusters of 8 run at once).  Trees of 8, us with 16 / 8: 151,669 entries and draft rows,
+    // 1 sequence 12.7 / 15.4, 9 sequences 22.5 / 24.3, 16 sequences 26.0 / 24.5; without draft rows 11.2 / 13.3,
+    // 14.5 / 15.1, 21.1 / 17.1; 32,000 entries, 1 sequence 10.1 / 10.1, 9 sequences 13.0 / 12.8.
+    const int cluster = vocab > 65536 && 16ll * d.B <= sm_count() && d.B <= wide ? 16 : 8;
     cfg.gridDim = dim3(static_cast<unsigned>(d.B) * cluster);
-    cfg.blockDim = dim3(oasis::kVerThreads);
-    cfg.dynamicSmemBytes = oasis::kVerSmem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, oasis::verify_tree_kernel, a);
     if (e != cudaSuccess) {
         cudaGetLastError();
