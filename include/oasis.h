@@ -433,9 +433,13 @@ int oasis_verify_tree(const oasis_dims* d, int32_t n_tree, int32_t vocab, const 
  * kmin, kmax, pool and slot_table are used; they are written (slot_table is
  * only read, and needs only its 4-byte alignment).  layers: host array.  k_tree, v_tree: bf16
  * [n_layers][B][Hkv][T][D].  If ctx_len_out is not NULL, ctx_len_out[b] =
- * ctx_len[b] + rows written (it must not alias ctx_len).  Positions at or
- * beyond N*P set OASIS_DEVERR_APPEND_FULL, path entries outside [0, T) and
- * n_accept outside [0, T] OASIS_DEVERR_ID_RANGE; such rows are skipped. */
+ * ctx_len[b] + the positions taken (it must not alias ctx_len): n_accept[b],
+ * cut to [0, T] (OASIS_DEVERR_ID_RANGE where that cuts) and to the room below
+ * N*P (OASIS_DEVERR_APPEND_FULL).  A path entry outside [0, T) sets
+ * OASIS_DEVERR_ID_RANGE and takes its position without writing: the rows
+ * behind it keep their places, and what the host block, the slot and the
+ * summary hold for that position stays as it was.  So after
+ * OASIS_DEVERR_ID_RANGE do not attend from ctx_len_out. */
 int oasis_commit_path(const oasis_dims* d, int32_t n_tree, const oasis_layer* layers, int32_t n_layers,
                       const void* k_tree, const void* v_tree, const int32_t* path, const int32_t* n_accept,
                       const int32_t* ctx_len, int32_t* ctx_len_out, void* stream);

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(
         int node = path[static_cast<long long>(b) * T + tid];
         if (node < 0 || node >= T) {
             raise_dev_error(OASIS_DEVERR_ID_RANGE);
-            node = -1;                             // its row is left as it was
+            node = -1;                             // its position is taken, and left as it was
         }
         s_node[tid] = node;
     }
