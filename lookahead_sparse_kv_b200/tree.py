@@ -201,6 +201,13 @@ def verify_tree(d: Dims, n_tree, probs, draft_probs, tokens, parent, n_nodes, u_
         raise _failed(rc, w)
 
 
+def _stack(x, what, name, dtype, layers, each, dev):
+    """_arg for a tensor stacked over layers, `each` elements a layer without a gap (further layers are not used)."""
+    if isinstance(x, torch.Tensor) and x.numel() > layers * each and x.numel() != x.shape[0] * each:
+        raise _bad(what, f"{name} must hold {each} elements a layer, got {tuple(x.shape)}")
+    return _arg(x, what, name, dtype, layers * each, dev)
+
+
 def make_cache_layers(d: Dims, host_kv, kmin, kmax, slot_table, pool):
     """oasis_layer table for commit_path from tensors stacked over layers: host_kv [L, B, Hkv, N, 2, 16, 128] (pinned; None
     where no host copy is kept), kmin / kmax [L, B, Hkv, N, 128], slot_table [L, B, Hkv, K], pool [L, B, Hkv, K, 2, 16, 128]
@@ -216,15 +223,15 @@ def make_cache_layers(d: Dims, host_kv, kmin, kmax, slot_table, pool):
     if L < 1:
         raise _bad(w, "no layers")
     N, K = d.max_blocks, d.budget_blocks
-    at = {"kmin": (_arg(kmin, w, "kmin", _BF16, L * units * N * 128, dev), units * N * 256),
-          "kmax": (_arg(kmax, w, "kmax", _BF16, L * units * N * 128, dev), units * N * 256)}
+    at = {"kmin": (_stack(kmin, w, "kmin", _BF16, L, units * N * 128, dev), units * N * 256),
+          "kmax": (_stack(kmax, w, "kmax", _BF16, L, units * N * 128, dev), units * N * 256)}
     if host_kv is not None:
         if host_kv.is_cuda:
             raise _bad(w, "host_kv must be pinned host memory")
-        at["host_kv"] = (_arg(host_kv, w, "host_kv", _BF16, L * units * N * 4096, -1), units * N * 8192)
+        at["host_kv"] = (_stack(host_kv, w, "host_kv", _BF16, L, units * N * 4096, -1), units * N * 8192)
     if pool is not None:
-        at["pool"] = (_arg(pool, w, "pool", _BF16, L * units * K * 4096, dev), units * K * 8192)
-        at["slot_table"] = (_arg(slot_table, w, "slot_table", _I32, L * units * K, dev), units * K * 4)
+        at["pool"] = (_stack(pool, w, "pool", _BF16, L, units * K * 4096, dev), units * K * 8192)
+        at["slot_table"] = (_stack(slot_table, w, "slot_table", _I32, L, units * K, dev), units * K * 4)
     table = (Layer * L)(*(Layer(**{name: base + i * step for name, (base, step) in at.items()}) for i in range(L)))
     table._keep = (host_kv, kmin, kmax, slot_table, pool)
     return table
