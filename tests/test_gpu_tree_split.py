@@ -121,3 +121,104 @@ def test_a_gather_runs_beside_a_split_call():
         share.append(ev[0].elapsed_time(ev[1]) / ev[0].elapsed_time(ev[2]))
     assert torch.equal(pool[:, :, :16].cpu(), host[:, :, :16])
     assert sorted(share[3:])[4] < 0.9, share
+
+
+@pytest.mark.parametrize("B,T,hq,hkv,K,kinds", [
+    # (KV tiles a unit = K / 8 and the tree's; on 148 SMs, 132 CTAs)
+    (64, 8, 8, 8, 24, ("full", "blind", "full", "free")),         # 512 items of 4 tiles: 4 whole ones a CTA
+    (39, 8, 16, 8, 128, ("full", "full", "free", "blind", "full")),   # 312 of 17: stretches of 41 over up to 4 items
+    (151, 40, 16, 2, 24, ("full", "free", "full")),               # pairs of row tiles, then single ones, whole
+    (20, 40, 16, 2, 128, ("full", "full", "blind")),              # the same, cut
+    (10, 64, 64, 8, 128, ("full", "free", "full", "full")),       # pairs alone, cut
+    (100, 33, 12, 4, 9, ("blind", "full")), (25, 64, 8, 8, 100, ("full",))])
+def test_many_segments_a_cta(B, T, hq, hkv, K, kinds):
+    """Both list buffers come round several times, segments without a tile lie between full ones, and CTAs pass from items of two row
+    tiles to items of one."""
+    Call(B, T, hq, hkv, K, seed=B + T, kinds=kinds).check()
+
+
+@pytest.mark.parametrize("T,hq", [(1, 1), (8, 4), (40, 16), (64, 16)])
+def test_items_of_many_parts(T, hq):
+    """One KV head over 1,024 slots: up to 65 parts to join, more than a warp has lanes."""
+    Call(1, T, hq, 1, 1024, seed=T).check()
+
+
+SPLIT = [(1, 7, 32, 8, 128), (2, 64, 16, 1, 1024)]
+
+
+def bits(c):
+    torch.cuda.synchronize()
+    return c.out.view(torch.int16).clone(), c.lse.view(torch.int32).clone()
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("shape", SPLIT)
+def test_split_calls_captured_on_one_workspace(shape):
+    """Two graphs on one workspace, replayed in turn on other inputs: the eager calls' bits, whatever the workspace held."""
+    first, second = Call(*shape, seed=1), Call(*shape, seed=2)
+    want = []
+    for c in (first, second):
+        c.run()
+        want.append(bits(c))
+    a, b = Call(*shape, seed=3), Call(*shape, seed=4)
+    graphs = []
+    torch.cuda.synchronize()
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(ws=a.ws)
+        graphs.append(g)
+    for c, src in ((a, first), (b, second)):
+        for n in ("q", "k", "v", "pool", "st", "ctx", "mask"):
+            getattr(c, n).copy_(getattr(src, n))
+    for _ in range(3):
+        a.ws.fill_(255)
+        for g in graphs:
+            g.replay()
+        assert same(bits(a), want[0]) and same(bits(b), want[1])
+
+
+@pytest.mark.parametrize("shape", SPLIT)
+def test_split_calls_on_two_streams(shape):
+    """Two calls at once, each with a workspace of its own, give what each gives alone; so do calls that follow one another closely."""
+    both = [Call(*shape, seed=s) for s in (5, 6)]
+    want = []
+    for c in both:
+        c.run()
+        want.append(bits(c))
+        c.out.zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(both, streams):
+            c.run(stream=s)
+    assert all(same(bits(c), w) for c, w in zip(both, want))
+    for _ in range(10):                                          # one stream, one workspace: the next call waits for the join
+        for c in both:
+            c.run(ws=both[0].ws)
+    assert all(same(bits(c), w) for c, w in zip(both, want))
+
+
+@pytest.mark.parametrize("shape", SPLIT)
+def test_split_calls_write_only_their_buffers(shape):
+    """Guard bands around a workspace of exactly the size asked for, and around the outputs."""
+    c = Call(*shape, seed=7)
+    c.run()
+    want = bits(c)
+    raw = {}
+    for n in ("ws", "out", "lse"):
+        t = getattr(c, n)
+        size = t.numel() * t.element_size()
+        raw[n] = torch.full((size + 2048,), 0xA5, dtype=torch.uint8, device=DEV)
+        setattr(c, n, raw[n][1024:1024 + size].view(t.dtype).view(t.shape))
+    inputs = [getattr(c, n) for n in ("q", "k", "v", "pool", "st", "ctx", "mask")]
+    kept = [t.clone() for t in inputs]
+    c.run()
+    assert same(bits(c), want)
+    for n, t in raw.items():
+        assert bool((t[:1024] == 0xA5).all()) and bool((t[-1024:] == 0xA5).all()), n
+    assert bool((raw["ws"][1024:-1024] != 0xA5).any())           # the parts went there
+    assert all(torch.equal(a, b) for a, b in zip(inputs, kept))
