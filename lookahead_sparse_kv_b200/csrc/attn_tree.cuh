@@ -31,13 +31,18 @@
 // Rounding.  Softmax weights are rounded to bf16 (2^-8 each, independent of one
 // another) because the value rows are bf16 and the MMA takes one type for both;
 // the sum of the weights is of the unrounded ones in fp32.  The output is
-// rounded to bf16 anyway, by as much again.
+// rounded to bf16 anyway, by as much again: 0.0023 from fp64 (relative, 16 x 8
+// nodes) where fp32 weights give 0.0017.  A remainder beside each weight in TMEM and
+// a second product with it give 0.0017 too, and take 36.7 us instead of 33.6 there,
+// 97 instead of 84 with 16 x 64 nodes.
 //
 // Work split.  The KV tiles of all items stand in one row (a unit's row tiles far
 // apart, so that they are worked on at the same time and DRAM gives the unit's
-// tiles once), and each CTA takes an equal stretch of it (`per` tiles), so every
-// SM has the same share whatever the number of items.  An item that lies in one stretch is written directly; the
-// parts of others go to the workspace, normalised, with their log2-sum-exp, and
+// tiles once), and each CTA takes an equal stretch of it (`per` tiles).  Where whole
+// items make a stretch at most four tiles longer it is rounded up to them, which can
+// leave CTAs without work (128 of 132 have some in both cases of 16 sequences below;
+// 16 SMs are left to the gather).  An item that lies in one stretch is written directly;
+// the parts of others go to the workspace, normalised, with their log2-sum-exp, and
 // a second kernel joins them, a warp a row.  (Joined by the item's last CTA
 // instead, 28 rows of 9 parts took 20 us: one SM for each item, all its loads
 // waiting for one another, and code that no SM had fetched yet.)
@@ -46,9 +51,12 @@
 // 64 / 8 heads, 128 slots a KV head, a tenth of them free: 33.5 us (the 142 MB that
 // are read at 5.8 TB/s while the tiles stream, 46,000 of 58,000 cycles; the rest is
 // the list, the first tile and the last epilogue); 16 x 64 nodes: 84 us, 0.84
-// PFLOP/s (the tensor core busy 44 % of the time, the softmax chain the limit: ~1,500
-// cycles a half tile for both warpgroups); one sequence x 7 nodes, 32 / 8 heads:
-// 16.6 us (latency: 8.5 us of attention, then the join).
+// PFLOP/s (the tensor pipe active in 34 % of all SMs' cycles of a cold launch of 96 us,
+// the softmax chain the limit: ~1,500 cycles a half tile for both warpgroups; 154 MB
+// read from DRAM, what there is to read); one sequence x 7 nodes, 32 / 8 heads: 16.7 us
+// (8.5 us of attention by 68 CTAs, then the join).  KV tiles are read evict-first:
+// 33.6 us where the default takes 35.3 (16 x 8) and 84.5 where it takes 85.0 (16 x 64);
+// one sequence's 8 MB, which L2 can hold from call to call, 16.6 where it takes 16.0.
 //
 // Roles (12 warps, mbarriers for every hand-off, every wait bounded):
 //   warps 0-3, 4-7  softmax of the even / odd steps and the epilogue

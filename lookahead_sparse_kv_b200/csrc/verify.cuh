@@ -26,8 +26,9 @@
 // another's; rows are read again for each sum, from L2.  HBM bounds it at many
 // sequences (the rows p and d of the last node, once), latency at one: the walk's
 // gathers, a share of the row and two cluster barriers.  32 trees of 26 nodes over
-// 151,669 entries: 31 us (up to four sums one after another, ~6 us each, of which the
-// first waits for HBM); one chain of 5 over 32,000: 7.5 us.
+// 151,669 entries: 33.6 us (up to four sums one after another, ~6 us each, of which the
+// first waits for HBM; 40 MB read); one chain of 5 over 32,000: 8.2 us; trees of 8 over
+// 151,669, one sequence 12.5 us, without draft rows 11.1 (a sum for the draw alone).
 #pragma once
 
 #include <cooperative_groups.h>
